@@ -263,6 +263,105 @@ int s2attn_graph_gap(const float* lse_s2, const float* lse_full, const void* o_s
                      int64_t B, int64_t N, int64_t H, int64_t D, int64_t G, int64_t n_valid, int variant,
                      float* rho, float* dist, float* stats, void* stream);
 
+/* Answering with a model: a paged cache of keys and values.  The inference
+ * graph (S2_DENSE_CAUSAL) attends from each new token to all earlier ones; the
+ * calls below keep the earlier tokens' keys and values in pages, so that a
+ * step reads them and computes nothing of them again.
+ *
+ * The cache.  k and v hold `pages` pages of page_size rows for each of `heads`
+ * key/value heads, [pages, heads, page_size, ..], contiguous, device memory,
+ * 16-byte aligned.  D in {64, 128}, page_size in {16, 32, 64, 128}.
+ *   S2_CACHE_BF16: rows of D bf16; k_scale and v_scale are NULL.
+ *   S2_CACHE_Q4:   rows of D/2 bytes, byte j = code(j) | code(j + D/2) << 4, and
+ *                  k_scale, v_scale [pages, heads, page_size, 2] bf16 with the
+ *                  row's {scale, min}: code c stands for min + scale·c.
+ * The batch.  Sequence b (of `seqs`) has seq_lens[b] tokens, the new ones of
+ * the call INCLUDED; the row at place p is in page page_table[b][p / page_size],
+ * slot p % page_size (page_table int32 [seqs, table_width]; entries behind a
+ * sequence's last page are not read).  The new tokens of all sequences lie on
+ * one packed axis of `tokens`: sequence b's are [q_starts[b], q_starts[b+1])
+ * (q_starts int32 [seqs + 1], non-decreasing); its new token i is at place
+ * seq_lens[b] - n_b + i.  q_starts = NULL: one new token per sequence.  All
+ * three arrays are device memory and are read when the kernels run, so a
+ * captured graph may be replayed with other lengths, starts and pages.
+ * A sequence with no new token takes no part; tokens before q_starts[0] or from
+ * q_starts[seqs] on belong to nobody and their outputs are left as they were.
+ * A new token whose place is negative (seq_lens[b] < n_b, as in a padded batch
+ * with seq_lens[b] = 0) has no row and sees no key: nothing is stored for it,
+ * its o is 0 and its lse -inf.
+ * max_new and max_len are the host's bounds of n_b and seq_lens[b]: they choose
+ * kernels and their tiling, and no result depends on them.
+ * Numbers out of range (a page outside [0, pages), a length beyond the table, a
+ * decreasing or too large start) are found by the kernels: nothing outside the
+ * buffers is touched, the sequence's results are undefined, and
+ * s2attn_check_status() reports S2_ERR_BOUNDS.
+ * Two sequences may share pages that are only read.  The rows of the calls'
+ * inputs must not overlap their outputs. */
+enum { S2_CACHE_BF16 = 0, S2_CACHE_Q4 = 1 };
+
+typedef struct {
+  void* k;
+  void* v;
+  void* k_scale; /* S2_CACHE_Q4 only */
+  void* v_scale;
+  int64_t pages;
+  int64_t heads; /* key/value heads */
+  int64_t page_size;
+  int64_t D;
+  int format;
+} s2_cache;
+
+typedef struct {
+  const int32_t* page_table; /* [seqs, table_width] */
+  const int32_t* seq_lens;   /* [seqs] */
+  const int32_t* q_starts;   /* [seqs + 1], or NULL: one new token per sequence */
+  int64_t seqs;
+  int64_t tokens;
+  int64_t table_width;
+  int64_t max_new; /* in [0, tokens]; 0: not known */
+  int64_t max_len; /* in [0, table_width * page_size]; 0: not known */
+} s2_cache_batch;
+
+/* Stores the new tokens' keys and values in their rows, keys rotated to their
+ * positions as s2attn_rope does (positions: int32 [tokens], or NULL = places;
+ * base, scale as there), and rotates the queries beside them: q [tokens,
+ * heads, D] -> q_out.  k, v: bf16 [tokens, cache heads, D].  The rows of a
+ * token are ldq, ldk, ldv elements apart (multiples of 8), so q, k and v may
+ * be parts of one projection's output; q_out is contiguous.  q and q_out may
+ * both be NULL.  base = 0 stores keys as they are (already rotated); q must
+ * then be NULL.  Into a 4-bit cache, each row x (rounded to bf16) gets
+ * min = min_j x_j, scale = bf16((max_j x_j - min) / 15), code_j =
+ * min(rint((x_j - min) / scale), 15), 0 when scale is 0; a row that holds an
+ * infinity or a NaN reads back as NaN.  Pages that other sequences share must
+ * not be written. */
+int s2attn_cache_append(const s2_cache* cache, const s2_cache_batch* batch, const void* q, int64_t ldq,
+                        const void* k, int64_t ldk, const void* v, int64_t ldv, void* q_out, int64_t heads,
+                        const int32_t* positions, double base, double scale, void* stream);
+
+/* The inverse: the rows of the batch's new tokens as bf16 k_out, v_out [tokens,
+ * cache heads, D] (from 4 bits min + scale·code, rounded once).  With n_b =
+ * seq_lens[b] it takes whole sequences out, as s2attn_fwd takes them.  Tokens
+ * without a row are left as they were. */
+int s2attn_cache_read(const s2_cache* cache, const s2_cache_batch* batch, void* k_out, void* v_out, void* stream);
+
+/* Attention of the new tokens over the cache (their own rows included: append
+ * first).  q [tokens, heads, D] bf16, rows of a token ldq elements apart, rotated;
+ * heads a multiple of the cache's, query head h reads key/value head
+ * h / (heads / cache heads).  For the token at place p of its sequence
+ *   o = sum_{j <= p} softmax_j(q·k_j / sqrt(D)) v_j,  lse = ln sum_{j <= p} exp(..),
+ * o [tokens, heads, D] bf16, lse [tokens, heads] fp32 or NULL.  Results do not
+ * depend on which other sequences are in the batch beyond the order of sums in
+ * 32 bits, and are bitwise reproducible for the same batch.  Rows behind a
+ * sequence's end may hold anything; a value row that is not finite makes NaN of
+ * every new token of its sequence that the call computes beside it, also of
+ * those before it.  workspace: s2attn_cache_attn_workspace_size bytes (0: the
+ * arguments are refused), 256-byte aligned, contents on entry do not matter;
+ * calls that may overlap on the GPU need one each. */
+size_t s2attn_cache_attn_workspace_size(const s2_cache* cache, const s2_cache_batch* batch, int64_t heads);
+
+int s2attn_cache_attn(const s2_cache* cache, const s2_cache_batch* batch, const void* q, int64_t ldq, void* o,
+                      float* lse, int64_t heads, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Size of the fixed scratch array behind s2attn_bwd_noalloc_v (32 MiB). */
 #define S2_NOALLOC_SCRATCH_BYTES (32u << 20)
 

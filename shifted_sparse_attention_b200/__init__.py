@@ -8,3 +8,6 @@ from .binding import (  # noqa: F401
     s2_attention, s2attn_bwd, s2attn_bwd_stages_v, s2attn_bwd_v, s2attn_bwd_workspace_size, s2attn_check_status,
     s2attn_debug_adjacency, s2attn_fwd, s2attn_fwd_v, s2attn_last_error,
 )
+from .cache import (  # noqa: F401
+    CacheBatch, KVCache, cache_append, cache_attention, cache_attention_workspace, cache_read,
+)

@@ -52,6 +52,11 @@ SIGNATURES = {
     "s2attn_sp_ds_workspace_size": ([_i64, _i64, _i64, _i64, _i64, _int, _int, _int], _sz),
     "s2attn_sp_halo_pack": ([_vp, _vp, _vp, _i64, _i64, _i64, _i64, _i64, _int, _vp], _int),
     "s2attn_sp_halo_unpack": ([_vp, _vp, _vp, _i64, _i64, _i64, _i64, _i64, _int, _vp], _int),
+    "s2attn_cache_append": ([_vp, _vp, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, ctypes.c_double,
+                             ctypes.c_double, _vp], _int),
+    "s2attn_cache_read": ([_vp, _vp, _vp, _vp, _vp], _int),
+    "s2attn_cache_attn_workspace_size": ([_vp, _vp, _i64], _sz),
+    "s2attn_cache_attn": ([_vp, _vp, _vp, _i64, _vp, _fp, _i64, _vp, _sz, _vp], _int),
     "s2attn_debug_adjacency": ([_i64, _i64, _i64, _int, _int, _int, _vp, _vp], _int),
     "s2attn_debug_adjacency_docs": ([_i64, _i64, _i64, _int, _int, _vp, _int, _vp, _vp], _int),
     "s2attn_check_status": ([_vp], _int),

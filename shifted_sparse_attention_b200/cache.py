@@ -1,0 +1,239 @@
+"""Answering with a model: the paged cache of keys and values (include/s2attn.h).
+
+A step appends its new tokens' keys and values and attends from the new tokens
+over everything their sequences hold:
+
+    cache = KVCache.empty(pages, page_size, heads, dim)          # bits=4 packs rows to 4 bits
+    batch = CacheBatch(page_table, seq_lens, q_starts, tokens)   # device int32 tensors
+    q = cache_append(cache, batch, k, v, q)                      # rotates q and k on the way
+    o = cache_attention(cache, batch, q)
+
+Argument marshalling only; the computation runs in libs2attn.so.  Tensors that
+a call allocates itself belong to the stream that it runs on.
+"""
+from __future__ import annotations
+
+import contextlib
+import ctypes
+
+import torch
+
+from . import binding
+from .binding import _check, _ptr, lib
+
+CACHE_BF16, CACHE_Q4 = 0, 1
+
+
+class _CacheStruct(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("pages", ctypes.c_int64), ("heads", ctypes.c_int64),
+                ("page_size", ctypes.c_int64), ("D", ctypes.c_int64), ("format", ctypes.c_int)]
+
+
+class _BatchStruct(ctypes.Structure):
+    _fields_ = [("page_table", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p), ("q_starts", ctypes.c_void_p),
+                ("seqs", ctypes.c_int64), ("tokens", ctypes.c_int64), ("table_width", ctypes.c_int64),
+                ("max_new", ctypes.c_int64), ("max_len", ctypes.c_int64)]
+
+
+class KVCache:
+    """Pages of keys and values: k, v bf16 [pages, heads, page_size, D], or for a 4-bit cache uint8
+    [pages, heads, page_size, D/2] with k_scale, v_scale bf16 [pages, heads, page_size, 2]."""
+
+    def __init__(self, k, v, k_scale=None, v_scale=None):
+        q4 = k_scale is not None
+        tensors = [k, v] + ([k_scale, v_scale] if q4 else [])
+        if (v_scale is not None) != q4:
+            raise ValueError("k_scale and v_scale go together")
+        for t in tensors:
+            if t.dim() != 4 or not t.is_cuda or not t.is_contiguous() or t.device != k.device:
+                raise ValueError("expected contiguous CUDA tensors [pages, heads, page_size, ..] on one device")
+        if any(t.dtype != (torch.uint8 if q4 else torch.bfloat16) for t in (k, v)) or v.shape != k.shape:
+            raise ValueError("k and v must be of one shape, bf16 (or uint8 codes with scales)")
+        if q4 and any(t.dtype != torch.bfloat16 or t.shape != (*k.shape[:3], 2) for t in (k_scale, v_scale)):
+            raise ValueError("k_scale and v_scale must be bf16 [pages, heads, page_size, 2]")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.pages, self.heads, self.page_size = (int(x) for x in k.shape[:3])
+        self.dim = int(k.shape[3]) * (2 if q4 else 1)
+        self.format = CACHE_Q4 if q4 else CACHE_BF16
+        self.device = k.device
+        self._struct = _CacheStruct(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), self.pages, self.heads,
+                                    self.page_size, self.dim, self.format)
+        self.address = ctypes.addressof(self._struct)
+
+    @classmethod
+    def empty(cls, pages: int, page_size: int, heads: int, dim: int, bits: int = 16, device="cuda"):
+        if bits not in (4, 16):
+            raise ValueError("bits must be 16 or 4")
+        shape, kind = (pages, heads, page_size, dim), torch.bfloat16
+        if bits == 4:
+            shape, kind = (pages, heads, page_size, dim // 2), torch.uint8
+        data = [torch.empty(shape, dtype=kind, device=device) for _ in range(2)]
+        scales = [torch.empty((*shape[:3], 2), dtype=torch.bfloat16, device=device) for _ in range(2 if bits == 4 else 0)]
+        return cls(*data, *scales)
+
+
+class CacheBatch:
+    """The sequences of a call: page_table int32 [seqs, width], seq_lens int32 [seqs] (new tokens included) and
+    q_starts int32 [seqs + 1], the packed starts of the new tokens (None: one per sequence), on the device;
+    tokens: length of the packed axis.  max_new, max_len: the host's bounds of a sequence's new tokens and length, if
+    known; they choose kernels and change no result.  The tensors' contents are read when kernels run: the same batch
+    serves step after step, and captured graphs, while the program updates them in place."""
+
+    def __init__(self, page_table, seq_lens, q_starts=None, tokens: int | None = None, max_new: int = 0,
+                 max_len: int = 0):
+        for t, dims in ((page_table, 2), (seq_lens, 1), (q_starts, 1)):
+            if t is not None and (t.dim() != dims or t.dtype != torch.int32 or not t.is_cuda or not t.is_contiguous()
+                                  or t.device != page_table.device):
+                raise ValueError("page_table [seqs, width], seq_lens [seqs] and q_starts [seqs + 1] must be contiguous "
+                                 "CUDA int32 tensors on one device")
+        seqs, width = (int(x) for x in page_table.shape)
+        if seq_lens.shape != (seqs,) or (q_starts is not None and q_starts.shape != (seqs + 1,)):
+            raise ValueError("page_table [seqs, width], seq_lens [seqs] and q_starts [seqs + 1] do not fit")
+        if tokens is None:
+            if q_starts is not None:
+                raise ValueError("with q_starts, tokens (the length of the packed axis) must be given")
+            tokens = seqs
+        self.page_table, self.seq_lens, self.q_starts = page_table, seq_lens, q_starts
+        self.seqs, self.tokens, self.device = seqs, int(tokens), page_table.device
+        self._struct = _BatchStruct(_ptr(page_table), _ptr(seq_lens), _ptr(q_starts), seqs, self.tokens, width,
+                                    int(max_new), int(max_len))
+        self.address = ctypes.addressof(self._struct)
+
+
+# ------------------------------------------------------------------ raw entry points (same names as the C ABI)
+
+
+def s2attn_cache_append(cache, batch, q, ldq, k, ldk, v, ldv, q_out, heads, positions, base, scale, stream=None) -> int:
+    return lib().s2attn_cache_append(cache.address, batch.address, _ptr(q), ldq, _ptr(k), ldk, _ptr(v), ldv,
+                                     _ptr(q_out), heads, _ptr(positions), base, scale, binding._stream(stream))
+
+
+def s2attn_cache_read(cache, batch, k_out, v_out, stream=None) -> int:
+    return lib().s2attn_cache_read(cache.address, batch.address, _ptr(k_out), _ptr(v_out), binding._stream(stream))
+
+
+def s2attn_cache_attn_workspace_size(cache, batch, heads) -> int:
+    return int(lib().s2attn_cache_attn_workspace_size(cache.address, batch.address, heads))
+
+
+def s2attn_cache_attn(cache, batch, q, ldq, o, lse, heads, workspace, workspace_bytes, stream=None) -> int:
+    return lib().s2attn_cache_attn(cache.address, batch.address, _ptr(q), ldq, _ptr(o), _ptr(lse), heads,
+                                   _ptr(workspace), workspace_bytes, binding._stream(stream))
+
+
+# ------------------------------------------------------------------ tensor-level helpers
+
+
+@contextlib.contextmanager
+def _on(device, stream):
+    """The cache's device and the call's stream as the current ones, so that what is allocated inside belongs to it."""
+    with torch.cuda.device(device):
+        if stream is None:
+            yield
+        else:
+            s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), device)
+            with torch.cuda.stream(s):
+                yield
+
+
+def _plain(cache, stream):
+    """Nothing to switch: the call runs on the current stream of the cache's device."""
+    return stream is None and cache.device.index == torch.cuda.current_device()
+
+
+def _rows(name, t, cache, batch, heads=None):
+    """Row stride of [tokens, heads, D] bf16 rows whose heads lie side by side."""
+    if t.dim() != 3 or t.dtype != torch.bfloat16 or t.device != cache.device:
+        raise ValueError("%s must be bf16 [tokens, heads, D] on the cache's device" % name)
+    T, H, D = t.shape
+    if T != batch.tokens or D != cache.dim or (heads is not None and H != heads):
+        raise ValueError("%s is %s for %d tokens and rows of %d" % (name, tuple(t.shape), batch.tokens, cache.dim))
+    st = t.stride()
+    if st[2] != 1 or (H > 1 and st[1] != D):
+        raise ValueError("the heads of a token of %s must lie side by side" % name)
+    return st[0] if T > 1 else max(st[0], H * D)
+
+
+def _same_device(cache, batch):
+    if batch.device != cache.device:
+        raise ValueError("the batch is on another device than the cache")
+
+
+def _whole(name, t, shape, cache, dtype=torch.bfloat16):
+    if t.shape != shape or t.dtype != dtype or t.device != cache.device or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous %s tensor %s on the cache's device" % (name, dtype, tuple(shape)))
+
+
+def cache_append(cache: KVCache, batch: CacheBatch, k, v, q=None, positions=None, base: float = 10000.0,
+                 scale: float = 1.0, out=None, stream=None):
+    """Stores the new tokens' keys (rotated to their positions) and values [tokens, cache.heads, D]; returns the
+    rotated queries if q [tokens, heads, D] is given.  base=0: the keys are stored as they are."""
+    if not _plain(cache, stream):
+        with _on(cache.device, stream):
+            return cache_append(cache, batch, k, v, q, positions, base, scale, out)
+    _same_device(cache, batch)
+    ldk, ldv = _rows("k", k, cache, batch, cache.heads), _rows("v", v, cache, batch, cache.heads)
+    ldq = heads = 0
+    if q is not None:
+        ldq, heads = _rows("q", q, cache, batch), q.shape[1]
+        if out is None:
+            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        else:
+            _whole("out", out, q.shape, cache)
+    elif out is not None:
+        raise ValueError("out goes with q")
+    if positions is not None:
+        _whole("positions", positions, (batch.tokens,), cache, torch.int32)
+    _check(s2attn_cache_append(cache, batch, q, ldq, k, ldk, v, ldv, out, heads, positions, float(base), float(scale)))
+    return out
+
+
+def cache_read(cache: KVCache, batch: CacheBatch, out=None, stream=None):
+    """The rows of the batch's new tokens back as bf16 (k, v) [tokens, cache.heads, D]; tokens without a row are left
+    as they were in ``out``, an optional preallocated pair."""
+    if not _plain(cache, stream):
+        with _on(cache.device, stream):
+            return cache_read(cache, batch, out)
+    _same_device(cache, batch)
+    shape = (batch.tokens, cache.heads, cache.dim)
+    if out is None:
+        k, v = (torch.empty(shape, dtype=torch.bfloat16, device=cache.device) for _ in range(2))
+    else:
+        k, v = out
+        _whole("out", k, shape, cache)
+        _whole("out", v, shape, cache)
+    _check(s2attn_cache_read(cache, batch, k, v))
+    return k, v
+
+
+def cache_attention_workspace(cache: KVCache, batch: CacheBatch, heads: int):
+    """A workspace for cache_attention, to keep over steps.  Calls that may overlap on the GPU need one each."""
+    n = s2attn_cache_attn_workspace_size(cache, batch, heads)
+    if n == 0:
+        raise ValueError("%d heads, this cache and this batch do not go together: %s" % (
+            heads, binding.s2attn_last_error()))
+    return torch.empty(n, dtype=torch.uint8, device=cache.device)
+
+
+def cache_attention(cache: KVCache, batch: CacheBatch, q, out=None, lse=None, workspace=None, stream=None):
+    """Attention of the new tokens' queries [tokens, heads, D] (rotated) over their sequences up to themselves; returns
+    o [tokens, heads, D].  lse: optional float32 [tokens, heads] to fill.  Without a workspace one is allocated."""
+    if not _plain(cache, stream):
+        with _on(cache.device, stream):
+            return cache_attention(cache, batch, q, out, lse, workspace)
+    _same_device(cache, batch)
+    ldq, heads = _rows("q", q, cache, batch), q.shape[1]
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    else:
+        _whole("out", out, q.shape, cache)
+    if lse is not None:
+        _whole("lse", lse, q.shape[:2], cache, torch.float32)
+    if workspace is None:
+        workspace = cache_attention_workspace(cache, batch, heads)
+    elif workspace.device != cache.device or not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous on the cache's device")
+    _check(s2attn_cache_attn(cache, batch, q, ldq, out, lse, heads, workspace,
+                             workspace.numel() * workspace.element_size()))
+    return out

@@ -1,0 +1,292 @@
+// s2_cache_append.cu -- filling a paged cache of keys and values, and reading
+// its rows back.
+//
+// Append: the new keys (and, beside them, the queries) are rotated to their
+// positions as in s2_rope.cu and keys and values go to their rows of the
+// cache, in bf16 or packed to 4 bits, in one pass over q, k and v: the pass
+// is bound by HBM (or, for a few tokens, by latency), so the rotation and the
+// packing ride along for free and no rotated copy of k is written.
+//
+// Work: a CTA takes kTok tokens.  Their places, pages and angles come first
+// (one warp per token finds its sequence, one thread per (token, pair) its
+// angle), then D/16 lanes take a row of one head: lane i the channels
+// [8i, 8i + 8) and [D/2 + 8i, D/2 + 8i + 8), which are 8 rotation pairs and, in
+// 4 bits, 8 bytes.  A 4-bit row needs its extremes before its codes: they
+// come from shuffles among those lanes, so the row is read once.
+//
+// The angle in turns, pos·scale·base^(-2j/D) / 2π, is formed and reduced to
+// [-1/2, 1/2] in 64 bits, its sine and cosine taken there and rounded to 32.
+// The rotation is done in 32 bits and rounded once to bf16.  4-bit codes are
+// made from the bf16 row, so both formats hold the same rotated row.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "s2_cache.cuh"
+#include "s2_kernels.h"
+
+namespace s2 {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kTok = 4;  // tokens of a CTA
+
+// Sequence of packed token t: the number of sequences whose new tokens end at or before t.
+// Whole warp; B when no sequence holds it.
+__device__ __forceinline__ int seq_of_token(const CacheArgs& c, int t, int lane) {
+  if (!c.starts) return t;
+  int n = 0;
+  for (int b = lane; b < c.B; b += 32) n += c.starts[b + 1] <= t;
+  return __reduce_add_sync(0xffffffffu, n);
+}
+
+// Places and pages of the CTA's tokens; place < 0 or ok false: nothing is stored.
+struct Token {
+  int place;
+  int page;
+  bool mine;   // belongs to a sequence
+  bool store;  // and has a row in the cache
+};
+
+__device__ __forceinline__ void find_tokens(const CacheArgs& c, int t0, Token* tok) {
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  if (warp < kTok) {
+    const int t = t0 + warp;
+    Token r{0, 0, false, false};
+    if (t < c.T) {
+      const int b = seq_of_token(c, t, lane);
+      if (b < c.B) {
+        const Seq s = load_seq(c, b);
+        if (t >= s.first && t - s.first < s.n) {
+          r.place = s.len - s.n + (t - s.first);
+          r.mine = true;
+          if (r.place >= 0) {
+            const int page = c.table[(size_t)b * c.width + (r.place >> c.log2s)];
+            r.store = (unsigned)page < (unsigned long long)c.pages;
+            r.page = r.store ? page : 0;
+            if (!r.store && lane == 0) atomicOr(c.status, kCacheFlag);
+          }
+        }
+      }
+    }
+    if (lane == 0) tok[warp] = r;
+  }
+}
+
+struct Row {
+  float lo[8], hi[8];  // channels [8i, 8i + 8) and [D/2 + 8i, ..)
+};
+
+__device__ __forceinline__ void unpack8(const uint4& raw, float* x) {
+  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(w[i] << 16);
+    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+
+__device__ __forceinline__ uint4 pack8(const float* x) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 p = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t*>(&p);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Packs a row held by LANES lanes (bf16 values) to 4 bits: this lane's 8 bytes and the row's (scale, min).
+// A row with a NaN or an infinity reads back as NaN.
+template <int LANES>
+__device__ __forceinline__ void pack_row(const Row& x, uint2& codes, uint32_t& pair) {
+  float mn = x.lo[0], mx = x.lo[0];
+  bool fine = true;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    mn = fminf(mn, fminf(x.lo[i], x.hi[i]));
+    mx = fmaxf(mx, fmaxf(x.lo[i], x.hi[i]));
+    fine = fine && isfinite(x.lo[i]) && isfinite(x.hi[i]);
+  }
+  int good = fine;
+#pragma unroll
+  for (int off = LANES / 2; off > 0; off >>= 1) {
+    mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, off));
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+    good &= __shfl_xor_sync(0xffffffffu, good, off);
+  }
+  // the scale is rounded to bf16 (8 bits) before the codes are chosen, so the rounding moves the grid
+  // (by 2^-9 of it, at most 0.03 of a step at its end) and not the error of a value
+  __nv_bfloat16 sb = __float2bfloat16_rn((mx - mn) / 15.0f);
+  __nv_bfloat16 mb = __float2bfloat16_rn(mn);  // exact: the row is bf16
+  const float s = __bfloat162float(sb);
+  uint32_t w[2] = {0u, 0u};
+  if (good && s > 0.f) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float lo = fminf(rintf(__fdiv_rn(x.lo[i] - mn, s)), 15.f);
+      const float hi = fminf(rintf(__fdiv_rn(x.hi[i] - mn, s)), 15.f);
+      w[i / 4] |= ((uint32_t)lo | ((uint32_t)hi << 4)) << (8 * (i % 4));
+    }
+  }
+  if (!good) sb = mb = __float2bfloat16_rn(NAN);
+  codes = make_uint2(w[0], w[1]);
+  pair = (uint32_t)__bfloat16_as_ushort(sb) | ((uint32_t)__bfloat16_as_ushort(mb) << 16);
+}
+
+}  // namespace
+
+// Rows of a token in order: H query heads (none without q), Hkv key heads, Hkv value heads.
+template <int D, bool Q4, bool kRotate>
+__global__ void __launch_bounds__(kThreads) s2_cache_append_kernel(const __grid_constant__ CacheArgs c,
+                                                                   const __grid_constant__ AppendIn in) {
+  constexpr int kHalf = D / 2, kLanes = D / 16, kRows = kThreads / kLanes;
+  __shared__ Token tok[kTok];
+  __shared__ float2 cs[kTok][kHalf];
+  const int t0 = blockIdx.x * kTok;
+  find_tokens(c, t0, tok);
+  __syncthreads();
+  if constexpr (kRotate) {
+    for (int i = threadIdx.x; i < kTok * kHalf; i += kThreads) {
+      const int x = i / kHalf, j = i % kHalf;
+      if (tok[x].mine) {
+        const int pos = in.positions ? in.positions[t0 + x] : tok[x].place;
+        const double turns = (double)pos * in.turns[j];
+        double s, co;
+        sincospi(2.0 * (turns - rint(turns)), &s, &co);
+        cs[x][j] = make_float2((float)co, (float)s);
+      }
+    }
+    __syncthreads();
+  }
+  const int per_token = in.q_heads + 2 * c.heads;
+  const int lane = threadIdx.x % kLanes;
+  const int total = kTok * per_token;
+  // whole warps go around together (the packing's shuffles need all lanes)
+  for (int w0 = 0; w0 < total; w0 += kRows) {
+    const int w = w0 + threadIdx.x / kLanes;
+    const int x = w / per_token, r = w % per_token;
+    const bool is_q = r < in.q_heads, is_v = r >= in.q_heads + c.heads;
+    const int h = is_q ? r : is_v ? r - in.q_heads - c.heads : r - in.q_heads;
+    const bool live = w < total && (is_q ? tok[x].mine : tok[x].store);
+    Row row;
+    if (live) {
+      const __nv_bfloat16* src = (is_q ? in.q + (size_t)(t0 + x) * in.ldq
+                                  : is_v ? in.v + (size_t)(t0 + x) * in.ldv
+                                         : in.k + (size_t)(t0 + x) * in.ldk) + (size_t)h * D + 8 * lane;
+      unpack8(*reinterpret_cast<const uint4*>(src), row.lo);
+      unpack8(*reinterpret_cast<const uint4*>(src + kHalf), row.hi);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) row.lo[i] = row.hi[i] = 0.f;
+    }
+    if (kRotate && live && !is_v) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float2 a = cs[x][8 * lane + i];
+        // products rounded one by one, as plain 32-bit arithmetic does it: a value at a rounding border
+        // must not depend on the compiler's choice, since 4-bit codes are made from it
+        const float lo = __fsub_rn(__fmul_rn(row.lo[i], a.x), __fmul_rn(row.hi[i], a.y));
+        const float hi = __fadd_rn(__fmul_rn(row.hi[i], a.x), __fmul_rn(row.lo[i], a.y));
+        row.lo[i] = lo;
+        row.hi[i] = hi;
+      }
+    }
+    const uint4 lo = pack8(row.lo), hi = pack8(row.hi);
+    if (!Q4 || is_q) {
+      if (live) {
+        __nv_bfloat16* dst = is_q ? in.q_out + ((size_t)(t0 + x) * in.q_heads + h) * D
+                                  : static_cast<__nv_bfloat16*>(is_v ? c.v : c.k) +
+                                        row_of(c, tok[x].page, h, tok[x].place) * D;
+        *reinterpret_cast<uint4*>(dst + 8 * lane) = lo;
+        *reinterpret_cast<uint4*>(dst + kHalf + 8 * lane) = hi;
+      }
+    }
+    if constexpr (Q4) {
+      unpack8(lo, row.lo);  // the row as bf16 holds it
+      unpack8(hi, row.hi);
+      uint2 codes;
+      uint32_t pair;
+      pack_row<kLanes>(row, codes, pair);
+      if (live && !is_q) {
+        const size_t at = row_of(c, tok[x].page, h, tok[x].place);
+        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(is_v ? c.v : c.k) + at * kHalf + 8 * lane) = codes;
+        if (lane == 0) static_cast<uint32_t*>(is_v ? c.v_scale : c.k_scale)[at] = pair;
+      }
+    }
+  }
+}
+
+// The inverse: rows of the batch's tokens, k and v [T, Hkv, D] in bf16 (one rounding from 4 bits).
+// Tokens of no sequence, or with no row in the cache, are left as they are.
+template <int D, bool Q4>
+__global__ void __launch_bounds__(kThreads) s2_cache_read_kernel(const __grid_constant__ CacheArgs c,
+                                                                 __nv_bfloat16* __restrict__ k_out,
+                                                                 __nv_bfloat16* __restrict__ v_out) {
+  constexpr int kHalf = D / 2, kLanes = D / 16, kRows = kThreads / kLanes;
+  __shared__ Token tok[kTok];
+  const int t0 = blockIdx.x * kTok;
+  find_tokens(c, t0, tok);
+  __syncthreads();
+  const int per_token = 2 * c.heads;
+  const int lane = threadIdx.x % kLanes;
+  for (int w = threadIdx.x / kLanes; w < kTok * per_token; w += kRows) {
+    const int x = w / per_token, r = w % per_token;
+    if (!tok[x].store) continue;
+    const bool is_v = r >= c.heads;
+    const int h = is_v ? r - c.heads : r;
+    const size_t at = row_of(c, tok[x].page, h, tok[x].place);
+    __nv_bfloat16* dst = (is_v ? v_out : k_out) + ((size_t)(t0 + x) * c.heads + h) * D;
+    uint4 lo, hi;
+    if constexpr (Q4) {
+      const uint2 codes =
+          *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(is_v ? c.v : c.k) + at * kHalf + 8 * lane);
+      const float2 p = q4_pair(static_cast<const uint32_t*>(is_v ? c.v_scale : c.k_scale)[at]);
+      Row row;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t b = ((i < 4 ? codes.x : codes.y) >> (8 * (i % 4))) & 0xffu;
+        // scale·code is exact (8 + 4 bits), so this is one rounding to 32 bits
+        row.lo[i] = fmaf(p.x, (float)(b & 15u), p.y);
+        row.hi[i] = fmaf(p.x, (float)(b >> 4), p.y);
+      }
+      lo = pack8(row.lo);
+      hi = pack8(row.hi);
+    } else {
+      const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(is_v ? c.v : c.k) + at * D + 8 * lane;
+      lo = *reinterpret_cast<const uint4*>(src);
+      hi = *reinterpret_cast<const uint4*>(src + kHalf);
+    }
+    *reinterpret_cast<uint4*>(dst + 8 * lane) = lo;
+    *reinterpret_cast<uint4*>(dst + kHalf + 8 * lane) = hi;
+  }
+}
+
+template <int D, bool Q4>
+static int append_impl(const CacheArgs& c, const AppendIn& in, bool rotate, cudaStream_t stream) {
+  const unsigned grid = (unsigned)((c.T + kTok - 1) / kTok);
+  if (rotate)
+    s2_cache_append_kernel<D, Q4, true><<<grid, kThreads, 0, stream>>>(c, in);
+  else
+    s2_cache_append_kernel<D, Q4, false><<<grid, kThreads, 0, stream>>>(c, in);
+  return (int)cudaGetLastError();
+}
+
+int launch_cache_append(const CacheArgs& c, const AppendIn& in, int D, bool q4, bool rotate, cudaStream_t stream) {
+  if (D == 64) return q4 ? append_impl<64, true>(c, in, rotate, stream) : append_impl<64, false>(c, in, rotate, stream);
+  return q4 ? append_impl<128, true>(c, in, rotate, stream) : append_impl<128, false>(c, in, rotate, stream);
+}
+
+template <int D, bool Q4>
+static int read_impl(const CacheArgs& c, void* k_out, void* v_out, cudaStream_t stream) {
+  s2_cache_read_kernel<D, Q4><<<(unsigned)((c.T + kTok - 1) / kTok), kThreads, 0, stream>>>(
+      c, static_cast<__nv_bfloat16*>(k_out), static_cast<__nv_bfloat16*>(v_out));
+  return (int)cudaGetLastError();
+}
+
+int launch_cache_read(const CacheArgs& c, int D, bool q4, void* k_out, void* v_out, cudaStream_t stream) {
+  if (D == 64) return q4 ? read_impl<64, true>(c, k_out, v_out, stream) : read_impl<64, false>(c, k_out, v_out, stream);
+  return q4 ? read_impl<128, true>(c, k_out, v_out, stream) : read_impl<128, false>(c, k_out, v_out, stream);
+}
+
+}  // namespace s2

@@ -1,0 +1,734 @@
+// s2_cache_attn.cu -- attention of a few new tokens over a paged cache.
+//
+// For new token t of sequence b at place p, head h of key/value head h / g:
+//     o = sum_{j <= p} softmax_j(q·k_j / sqrt(D)) v_j,   lse = ln sum exp.
+// From a 4-bit cache, with k_j = mk + sk·ck and codes centred, c' = c - 8
+// (exact in bf16):
+//     q·k_j       = sk (q·c'_j) + (mk + 8 sk) sum(q),
+//     sum p_j v_j = sum (p_j sv_j) c'_j + sum p_j (mv_j + 8 sv_j),
+// so the matrix products see whole numbers and nothing of a row is rounded.
+//
+// Bound: HBM (each row of the cache is read once, and serves the g·n rows of
+// queries that share it).  Everything else is arranged around keeping loads
+// in flight:
+// - a unit is (sequence, key/value head, block of 8·NR query rows); its keys
+//   are cut into steps of kStep keys.  All units' steps form one line, cut
+//   into equal pieces, one per CTA, so sequences of any lengths load all SMs
+//   alike; a unit cut by a border leaves partial sums (max, sum, O) that
+//   s2_cache_join adds up in a fixed order.
+// - a warp takes every fourth step of its CTA's piece by itself: loads go from
+//   global memory straight to the registers that mma.sync reads as its A
+//   operand (S^T = K Q^T and O^T = V^T P^T, so keys fill the 16-row side and
+//   the few query rows the 8-column side), with no shared memory and no
+//   barrier in the loop.  K of the next step is asked for when this step's
+//   scores are done, V when its products are.
+// - channels and keys may come in any order inside a product as long as both
+//   operands agree, so every lane loads 16 contiguous bytes (8 in 4 bits) of a
+//   row; V's pairs along the keys are put together with byte permutes, the
+//   weights' with one 8x8 transposition (movmatrix).
+// - the running maximum moves only when a score passes it by more than 8 (a
+//   factor 256), which one vote per step tells; sums are in 32 bits, the
+//   weights are rounded to bf16 for the product (relative 2^-9 each, independent
+//   signs) and added up unrounded.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "s2_cache.cuh"
+#include "s2_kernels.h"
+#include "sm100_ptx.cuh"
+
+namespace s2 {
+
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
+
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+// Two codes (bits [0,4) and [16,20) of x) as bf16 code - 8: 0x4300 | c is 128 + c.
+__device__ __forceinline__ uint32_t codes_bf16(uint32_t x) {
+  const uint32_t y = (x & 0x000f000fu) | 0x43004300u;
+  const __nv_bfloat162 off = __halves2bfloat162(__ushort_as_bfloat16(0x4308), __ushort_as_bfloat16(0x4308));
+  const __nv_bfloat162 z = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&y), off);
+  return *reinterpret_cast<const uint32_t*>(&z);
+}
+
+// The caches are read once: past L1, and first to leave L2.
+__device__ __forceinline__ uint4 ld_stream16(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint2 ld_stream8(const void* p) {
+  uint2 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint32_t ld_stream4(const void* p) {
+  uint32_t v;
+  asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
+
+// Registers of one 16-key block of K and of V in the order the products take them.
+template <int D, bool Q4>
+struct KeyRegs;
+template <int D>
+struct KeyRegs<D, false> {
+  uint4 w[D / 32][2];  // [32-channel block][key r / r + 8]: channels 32i + 8c ..
+};
+template <int D>
+struct KeyRegs<D, true> {
+  uint32_t w[2][D / 32];  // [key r / r + 8]: D/8 bytes from byte (D/8)c
+  uint32_t pair[2];
+};
+template <int D, bool Q4>
+struct ValueRegs;
+template <int D>
+struct ValueRegs<D, false> {
+  uint4 w[4][D / 64];  // [key 2c, 2c+1, 2c+8, 2c+9][64-channel block]: channels 64i + 8r ..
+};
+template <int D>
+struct ValueRegs<D, true> {
+  uint32_t w[4][D / 64];  // D/16 bytes from byte (D/16)r
+  uint32_t pair[2];       // of keys r, r + 8
+};
+
+template <int D, bool Q4>
+__device__ __forceinline__ void load_keys(KeyRegs<D, Q4>& x, const CacheArgs& c, size_t row, int r, int cc) {
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const size_t at = row + r + 8 * u;
+    if constexpr (Q4) {
+      const uint8_t* p = static_cast<const uint8_t*>(c.k) + at * (D / 2) + (D / 8) * cc;
+      if constexpr (D == 128) {
+        const uint4 v = ld_stream16(p);
+        x.w[u][0] = v.x, x.w[u][1] = v.y, x.w[u][2] = v.z, x.w[u][3] = v.w;
+      } else {
+        const uint2 v = ld_stream8(p);
+        x.w[u][0] = v.x, x.w[u][1] = v.y;
+      }
+      x.pair[u] = ld_stream4(static_cast<const uint32_t*>(c.k_scale) + at);
+    } else {
+      const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(c.k) + at * D + 8 * cc;
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) x.w[i][u] = ld_stream16(p + 32 * i);
+    }
+  }
+}
+
+template <int D, bool Q4>
+__device__ __forceinline__ void load_values(ValueRegs<D, Q4>& x, const CacheArgs& c, size_t row, int r, int cc) {
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const size_t at = row + 2 * cc + (u & 1) + 8 * (u >> 1);
+    if constexpr (Q4) {
+      const uint8_t* p = static_cast<const uint8_t*>(c.v) + at * (D / 2) + (D / 16) * r;
+      if constexpr (D == 128) {
+        const uint2 v = ld_stream8(p);
+        x.w[u][0] = v.x, x.w[u][1] = v.y;
+      } else {
+        x.w[u][0] = ld_stream4(p);
+      }
+    } else {
+      const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(c.v) + at * D + 8 * r;
+#pragma unroll
+      for (int i = 0; i < D / 64; ++i) x.w[u][i] = ld_stream16(p + 64 * i);
+    }
+  }
+  if constexpr (Q4) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) x.pair[u] = ld_stream4(static_cast<const uint32_t*>(c.v_scale) + row + r + 8 * u);
+  }
+}
+
+// Channel of row `r` (+ 8 when hi) of O^T's tile j: the order in which V's lanes load.
+template <int D, bool Q4>
+__device__ __forceinline__ int channel_of(int j, bool hi, int r) {
+  if constexpr (Q4) return (D / 16) * r + j + (hi ? D / 2 : 0);
+  if constexpr (D == 128) return 8 * r + j + (hi ? 64 : 0);
+  return 8 * r + j + (hi ? 4 : 0);
+}
+
+// Steps of a unit of a sequence of len tokens; one for an empty sequence, whose rows are then written empty.
+__host__ __device__ constexpr int steps_of(int len, int step) { return len > 0 ? (len + step - 1) / step : 1; }
+
+// One block of query rows: units of sequence b are (kv head, block of 8·NR rows).
+template <int NR>
+__device__ __forceinline__ int row_blocks(int n, int g) {
+  return (int)(((long long)n * g + 8 * NR - 1) / (8 * NR));
+}
+
+// Where the line of all steps is cut, and the sequence that holds a given step of it.
+struct Line {
+  long long total, piece;
+};
+
+// Sum over the CTA's threads; all threads get it.
+__device__ __forceinline__ long long cta_sum(long long v, long long* sh) {
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+  __syncthreads();
+  if (threadIdx.x % 32 == 0) sh[threadIdx.x / 32] = v;
+  __syncthreads();
+  long long s = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) s += sh[w];
+  return s;
+}
+
+template <int NR>
+__device__ __forceinline__ long long seq_steps(const CacheArgs& c, const AttnIn& in, int b, int step) {
+  const Seq s = load_seq(c, b);
+  return (long long)c.heads * row_blocks<NR>(s.n, in.g) * steps_of(s.len, step);
+}
+
+template <int NR>
+__device__ __forceinline__ Line make_line(const CacheArgs& c, const AttnIn& in, int step, long long* sh) {
+  long long mine = 0;
+  for (int b = threadIdx.x; b < c.B; b += kThreads) mine += seq_steps<NR>(c, in, b, step);
+  Line l;
+  l.total = cta_sum(mine, sh);
+  l.piece = (l.total + in.pieces - 1) / in.pieces;
+  if (l.piece < in.min_piece) l.piece = in.min_piece;
+  return l;
+}
+
+// Sequence that holds step x of the line, and the line's first step of it (all threads; sh: kWarps + 2 values).
+template <int NR>
+__device__ __forceinline__ void find_seq(const CacheArgs& c, const AttnIn& in, int step, long long x, long long* sh,
+                                         int& b_out, long long& first_out) {
+  long long before = 0;
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  for (int b0 = 0; b0 < c.B; b0 += kThreads) {
+    const int b = b0 + threadIdx.x;
+    const long long mine = b < c.B ? seq_steps<NR>(c, in, b, step) : 0;
+    long long upto = mine;  // inclusive sum over the warp
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, upto, off);
+      if (lane >= off) upto += y;
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) sh[kWarps] = -1;
+    if (lane == 31) sh[warp] = upto;
+    __syncthreads();
+    long long base = before, all = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) base += sh[w];
+      all += sh[w];
+    }
+    const long long end = base + upto;
+    if (x < end && x >= end - mine) {
+      sh[kWarps] = b;
+      sh[kWarps + 1] = end - mine;
+    }
+    __syncthreads();
+    if (sh[kWarps] >= 0) {
+      b_out = (int)sh[kWarps];
+      first_out = sh[kWarps + 1];
+      return;
+    }
+    before += all;
+  }
+  b_out = -1;
+  first_out = 0;
+}
+
+}  // namespace
+
+// Partial sums of a piece's unit: per row D floats of O, then max and sum.
+template <int D>
+__host__ __device__ constexpr int partial_floats(int rows) {
+  return rows * (D + 2);
+}
+
+template <int D, bool Q4, int NR>
+__global__ void __launch_bounds__(kThreads, NR == 1 ? 4 : 2)
+    s2_cache_decode_kernel(const __grid_constant__ CacheArgs c, const __grid_constant__ AttnIn in) {
+  constexpr int kBlocks = Q4 ? 2 : 1;     // 16-key blocks of a step
+  constexpr int kStep = 16 * kBlocks;
+  constexpr int kRows = 8 * NR;
+  constexpr int kTiles = D / 16;          // 16-channel tiles of O^T
+  __shared__ long long sh[kWarps + 2];
+  __shared__ float s_o[kWarps][kRows][D + 4];
+  __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows];
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, r = lane / 4, cc = lane % 4;
+
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join may start its own set-up
+  const Line line = make_line<NR>(c, in, kStep, sh);
+  const long long x0 = line.piece * blockIdx.x;
+  if (x0 >= line.total) return;
+  const long long x1 = min(x0 + line.piece, line.total);
+  int b;
+  long long seq_first;
+  find_seq<NR>(c, in, kStep, x0, sh, b, seq_first);
+
+  long long x = x0;
+  while (x < x1) {
+    Seq seq = load_seq(c, b);
+    const int blocks = row_blocks<NR>(seq.n, in.g);
+    const int steps = steps_of(seq.len, kStep);
+    if (x >= seq_first + (long long)c.heads * blocks * steps) {  // this sequence is done
+      seq_first += (long long)c.heads * blocks * steps;
+      ++b;
+      continue;
+    }
+    const long long unit = (x - seq_first) / steps;
+    const long long unit_first = seq_first + unit * steps;
+    const int h = (int)(unit / blocks), rb = (int)(unit % blocks);
+    const int k0 = (int)(x - unit_first);
+    const int k1 = (int)min((long long)steps, x1 - unit_first);
+    const bool whole = k0 == 0 && k1 == steps;
+
+    // ---------------------------------------------------------- query rows
+    // B operand of S^T: lane (r, cc) holds row r's channels as load_keys orders them
+    uint32_t qf[NR][D / 16][2];
+    float qsum[NR][2];
+    int lim[NR][2];     // keys that the lane's two columns see
+    int lim_all = seq.len;  // keys that every row sees
+#pragma unroll
+    for (int y = 0; y < NR; ++y) {
+      const int row = rb * kRows + y * 8 + r;
+      const bool live = row < seq.n * in.g;
+      const __nv_bfloat16* p = in.q + (size_t)(seq.first + (live ? row / in.g : 0)) * in.ldq +
+                               (size_t)(h * in.g + (live ? row % in.g : 0)) * D;
+      float sum = 0.f;
+      if constexpr (Q4) {
+#pragma unroll
+        for (int half = 0; half < 2; ++half)
+#pragma unroll
+          for (int w = 0; w < D / 32; ++w) {
+            uint2 v = make_uint2(0u, 0u);
+            if (live) v = *reinterpret_cast<const uint2*>(p + half * (D / 2) + (D / 8) * cc + 4 * w);
+            // bytes 0, 2 and 1, 3 of a word of codes are taken together
+            qf[y][2 * w + half][0] = __byte_perm(v.x, v.y, 0x5410);
+            qf[y][2 * w + half][1] = __byte_perm(v.x, v.y, 0x7632);
+            sum += __uint_as_float(v.x << 16) + __uint_as_float(v.x & 0xffff0000u) + __uint_as_float(v.y << 16) +
+                   __uint_as_float(v.y & 0xffff0000u);
+          }
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) qsum[y][e] = __shfl_sync(0xffffffffu, sum, (2 * cc + e) * 4);
+      } else {
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+          uint4 v = make_uint4(0u, 0u, 0u, 0u);
+          if (live) v = *reinterpret_cast<const uint4*>(p + 32 * i + 8 * cc);
+          qf[y][2 * i][0] = v.x, qf[y][2 * i][1] = v.y, qf[y][2 * i + 1][0] = v.z, qf[y][2 * i + 1][1] = v.w;
+        }
+        qsum[y][0] = qsum[y][1] = 0.f;
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int col = rb * kRows + y * 8 + 2 * cc + e;
+        // rows of no token see every key; what they compute is not stored
+        lim[y][e] = col < seq.n * in.g ? max(0, seq.len - seq.n + col / in.g + 1) : seq.len;
+        lim_all = min(lim_all, lim[y][e]);
+      }
+    }
+    lim_all = min(lim_all, __shfl_xor_sync(0xffffffffu, lim_all, 1));
+    lim_all = min(lim_all, __shfl_xor_sync(0xffffffffu, lim_all, 2));
+
+    // ---------------------------------------------------------- keys
+    float acc[NR][kTiles][4];
+    float m[NR][2], l[NR][2], vsum[NR][2];
+#pragma unroll
+    for (int y = 0; y < NR; ++y) {
+#pragma unroll
+      for (int j = 0; j < kTiles; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[y][j][i] = 0.f;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) m[y][e] = -INFINITY, l[y][e] = 0.f, vsum[y][e] = 0.f;
+    }
+
+    KeyRegs<D, Q4> kr[kBlocks];
+    ValueRegs<D, Q4> vr[kBlocks];
+    size_t rows[kBlocks];
+    int k = k0 + warp;
+    // a block behind the last key is read from the last block instead: it lies in a page of the sequence
+    auto find_rows = [&](int step) {
+#pragma unroll
+      for (int u = 0; u < kBlocks; ++u) {
+        const int p = min(step * kStep + 16 * u, (seq.len - 1) & ~15);
+        rows[u] = row_of(c, page_of(c, b, p), h, p);
+      }
+    };
+    if (seq.len > 0 && k < k1) {
+      find_rows(k);
+#pragma unroll
+      for (int u = 0; u < kBlocks; ++u) load_keys(kr[u], c, rows[u], r, cc);
+#pragma unroll
+      for (int u = 0; u < kBlocks; ++u) load_values(vr[u], c, rows[u], r, cc);
+      for (; k < k1; k += kWarps) {
+        const int key0 = k * kStep;
+        const bool more = k + kWarps < k1;
+        if (more) find_rows(k + kWarps);
+        // scores: keys r, r + 8 of each block by rows 2cc, 2cc + 1
+        float s[NR][kBlocks][4];
+#pragma unroll
+        for (int u = 0; u < kBlocks; ++u) {
+#pragma unroll
+          for (int y = 0; y < NR; ++y) s[y][u][0] = s[y][u][1] = s[y][u][2] = s[y][u][3] = 0.f;
+          if constexpr (Q4) {
+#pragma unroll
+            for (int w = 0; w < D / 32; ++w)
+#pragma unroll
+              for (int half = 0; half < 2; ++half) {
+                const uint32_t a0 = codes_bf16(kr[u].w[0][w] >> (4 * half));
+                const uint32_t a1 = codes_bf16(kr[u].w[1][w] >> (4 * half));
+                const uint32_t a2 = codes_bf16(kr[u].w[0][w] >> (4 * half + 8));
+                const uint32_t a3 = codes_bf16(kr[u].w[1][w] >> (4 * half + 8));
+                // a word's bytes 0, 2 are channels 4w, 4w + 2: qf's first pair
+#pragma unroll
+                for (int y = 0; y < NR; ++y) {
+                  const uint32_t q01 = qf[y][2 * w + half][0], q23 = qf[y][2 * w + half][1];
+                  mma16816(s[y][u], a0, a1, a2, a3, q01, q23);
+                }
+              }
+          } else {
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) {
+              const uint4 a = kr[u].w[i][0], d = kr[u].w[i][1];
+#pragma unroll
+              for (int y = 0; y < NR; ++y) {
+                mma16816(s[y][u], a.x, d.x, a.y, d.y, qf[y][2 * i][0], qf[y][2 * i][1]);
+                mma16816(s[y][u], a.z, d.z, a.w, d.w, qf[y][2 * i + 1][0], qf[y][2 * i + 1][1]);
+              }
+            }
+          }
+          if constexpr (Q4) {
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              const float2 pr = q4_pair(kr[u].pair[t]);
+              const float mid = fmaf(8.f, pr.x, pr.y);
+#pragma unroll
+              for (int y = 0; y < NR; ++y)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) s[y][u][2 * t + e] = fmaf(s[y][u][2 * t + e], pr.x, mid * qsum[y][e]);
+            }
+          }
+        }
+        if (more) {
+#pragma unroll
+          for (int u = 0; u < kBlocks; ++u) load_keys(kr[u], c, rows[u], r, cc);
+        }
+        // masks, only where some row or the sequence ends in the step
+        if (key0 + kStep > lim_all) {
+#pragma unroll
+          for (int u = 0; u < kBlocks; ++u) {
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              const int key = key0 + 16 * u + r + 8 * t;
+#pragma unroll
+              for (int y = 0; y < NR; ++y)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                  if (key >= lim[y][e]) s[y][u][2 * t + e] = -INFINITY;
+              if constexpr (Q4) {
+                if (key >= seq.len) vr[u].pair[t] = 0u;
+              }
+            }
+            // rows behind the sequence hold anything; their weight is 0 and must stay so
+            if constexpr (!Q4) {
+#pragma unroll
+              for (int t = 0; t < 4; ++t)
+                if (key0 + 16 * u + 2 * cc + (t & 1) + 8 * (t >> 1) >= seq.len) {
+#pragma unroll
+                  for (int i = 0; i < D / 64; ++i) vr[u].w[t][i] = make_uint4(0u, 0u, 0u, 0u);
+                }
+            }
+          }
+        }
+        // running maximum
+        bool up = false;
+        float top[NR][2];
+#pragma unroll
+        for (int y = 0; y < NR; ++y)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float t = fmaxf(s[y][0][e], s[y][0][2 + e]);
+#pragma unroll
+            for (int u = 1; u < kBlocks; ++u) t = fmax3(t, s[y][u][e], s[y][u][2 + e]);
+            top[y][e] = t * in.scale_log2;
+            up = up || top[y][e] > m[y][e] + 8.f;
+          }
+        if (__any_sync(0xffffffffu, up)) {
+#pragma unroll
+          for (int y = 0; y < NR; ++y)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float t = top[y][e];
+#pragma unroll
+              for (int off = 4; off < 32; off <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, off));
+              t = fmaxf(t, m[y][e]);
+              const float f = t == -INFINITY ? 1.f : ex2(m[y][e] - t);
+              m[y][e] = t;
+              l[y][e] *= f;
+              vsum[y][e] *= f;
+#pragma unroll
+              for (int j = 0; j < kTiles; ++j) acc[y][j][e] *= f, acc[y][j][2 + e] *= f;
+            }
+        }
+        // weights, and O^T += V^T P^T
+#pragma unroll
+        for (int u = 0; u < kBlocks; ++u) {
+          uint32_t pf[NR][2];
+#pragma unroll
+          for (int y = 0; y < NR; ++y)
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              float w[2];
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const float base = m[y][e] == -INFINITY ? 0.f : m[y][e];
+                w[e] = ex2(fmaf(s[y][u][2 * t + e], in.scale_log2, -base));
+                l[y][e] += w[e];
+              }
+              if constexpr (Q4) {
+                const float2 pr = q4_pair(vr[u].pair[t]);
+                const float mid = fmaf(8.f, pr.x, pr.y);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  vsum[y][e] = fmaf(w[e], mid, vsum[y][e]);
+                  w[e] *= pr.x;
+                }
+              }
+              pf[y][t] = transpose8x8(pack_bf16(w[0], w[1]));
+            }
+          if constexpr (Q4) {
+#pragma unroll
+            for (int w = 0; w < D / 64; ++w)
+#pragma unroll
+              for (int q = 0; q < 2; ++q) {
+                const uint32_t lo = __byte_perm(vr[u].w[0][w], vr[u].w[1][w], q ? 0x7632 : 0x5410);
+                const uint32_t hi = __byte_perm(vr[u].w[2][w], vr[u].w[3][w], q ? 0x7632 : 0x5410);
+#pragma unroll
+                for (int z = 0; z < 2; ++z) {
+                  const int j = 4 * w + 2 * q + z;
+                  const uint32_t a0 = codes_bf16(lo >> (8 * z)), a1 = codes_bf16(lo >> (8 * z + 4));
+                  const uint32_t a2 = codes_bf16(hi >> (8 * z)), a3 = codes_bf16(hi >> (8 * z + 4));
+#pragma unroll
+                  for (int y = 0; y < NR; ++y) mma16816(acc[y][j], a0, a1, a2, a3, pf[y][0], pf[y][1]);
+                }
+              }
+          } else {
+#pragma unroll
+            for (int j = 0; j < kTiles; ++j) {
+              // the two channels of the tile's rows r and r + 8
+              constexpr int kHiAt = D == 128 ? 0 : 4;
+              const int e0 = j, e1 = j + kHiAt;
+              auto word = [&](int t, int block, int e) -> uint32_t {
+                const uint4& v = vr[u].w[t][block];
+                return e / 2 == 0 ? v.x : e / 2 == 1 ? v.y : e / 2 == 2 ? v.z : v.w;
+              };
+              constexpr int kHiBlock = D == 128 ? 1 : 0;
+              const uint32_t a0 = __byte_perm(word(0, 0, e0), word(1, 0, e0), e0 % 2 ? 0x7632 : 0x5410);
+              const uint32_t a1 = __byte_perm(word(0, kHiBlock, e1), word(1, kHiBlock, e1), e1 % 2 ? 0x7632 : 0x5410);
+              const uint32_t a2 = __byte_perm(word(2, 0, e0), word(3, 0, e0), e0 % 2 ? 0x7632 : 0x5410);
+              const uint32_t a3 = __byte_perm(word(2, kHiBlock, e1), word(3, kHiBlock, e1), e1 % 2 ? 0x7632 : 0x5410);
+#pragma unroll
+              for (int y = 0; y < NR; ++y) mma16816(acc[y][j], a0, a1, a2, a3, pf[y][0], pf[y][1]);
+            }
+          }
+        }
+        if (more) {
+#pragma unroll
+          for (int u = 0; u < kBlocks; ++u) load_values(vr[u], c, rows[u], r, cc);
+        }
+      }
+    }
+
+    // ---------------------------------------------------------- the warps' sums, joined
+#pragma unroll
+    for (int y = 0; y < NR; ++y)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) {
+          l[y][e] += __shfl_xor_sync(0xffffffffu, l[y][e], off);
+          vsum[y][e] += __shfl_xor_sync(0xffffffffu, vsum[y][e], off);
+        }
+        const int row = y * 8 + 2 * cc + e;
+#pragma unroll
+        for (int j = 0; j < kTiles; ++j) {
+          s_o[warp][row][channel_of<D, Q4>(j, false, r)] = acc[y][j][e] + vsum[y][e];
+          s_o[warp][row][channel_of<D, Q4>(j, true, r)] = acc[y][j][2 + e] + vsum[y][e];
+        }
+        if (r == 0) {
+          s_m[warp][row] = m[y][e];
+          s_l[warp][row] = l[y][e];
+        }
+      }
+    __syncthreads();
+    // four channels of a row a thread; rows of no token are left out
+    const int rows_here = min(kRows, seq.n * in.g - rb * kRows);
+    float* part = in.partial + (size_t)(2 * blockIdx.x + (x == x0 ? 0 : 1)) * partial_floats<D>(kRows);
+    for (int i = threadIdx.x; i < rows_here * (D / 4); i += kThreads) {
+      const int row = i / (D / 4), d = 4 * (i % (D / 4));
+      float mm = s_m[0][row];
+#pragma unroll
+      for (int w = 1; w < kWarps; ++w) mm = fmaxf(mm, s_m[w][row]);
+      float ll = 0.f;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        if (s_m[w][row] == -INFINITY) continue;
+        const float f = ex2(s_m[w][row] - mm);
+        const float4 v = *reinterpret_cast<const float4*>(&s_o[w][row][d]);
+        ll += s_l[w][row] * f;
+        o.x += v.x * f, o.y += v.y * f, o.z += v.z * f, o.w += v.w * f;
+      }
+      if (whole) {
+        const int at = rb * kRows + row;
+        const size_t out = (size_t)(seq.first + at / in.g) * in.heads + h * in.g + at % in.g;
+        const float inv = ll > 0.f ? 1.f / ll : 0.f;
+        *reinterpret_cast<uint2*>(in.o + out * D + d) =
+            make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+        if (in.lse && d == 0) in.lse[out] = ll > 0.f ? (mm + log2f(ll)) * 0.69314718055994531f : -INFINITY;
+      } else {
+        *reinterpret_cast<float4*>(part + row * D + d) = o;
+        if (d == 0) {
+          part[kRows * D + 2 * row] = mm;
+          part[kRows * D + 2 * row + 1] = ll;
+        }
+      }
+    }
+    __syncthreads();
+    x = unit_first + k1;
+  }
+}
+
+// Joins the partial sums of units that the line's cuts run through.  CTA i
+// stands for cut i + 1; the CTAs of one unit's cuts share its rows and
+// channels out among them.  The order of the sum is the pieces'.
+template <int D, bool Q4, int NR>
+__global__ void __launch_bounds__(kThreads) s2_cache_join_kernel(const __grid_constant__ CacheArgs c,
+                                                                 const __grid_constant__ AttnIn in) {
+  constexpr int kStep = Q4 ? 32 : 16;
+  constexpr int kRows = 8 * NR;
+  constexpr int kGroups = kThreads / 8;  // partial sums added side by side, 8 lanes of 4 channels each
+  __shared__ long long sh[kWarps + 2];
+  __shared__ float s_red[2][kWarps];
+  __shared__ float4 s_o[kGroups][8];
+  const Line line = make_line<NR>(c, in, kStep, sh);
+  const long long cut = line.piece * (blockIdx.x + 1);
+  if (cut >= line.total) return;
+  int b;
+  long long seq_first;
+  find_seq<NR>(c, in, kStep, cut, sh, b, seq_first);
+  const Seq seq = load_seq(c, b);
+  const int steps = steps_of(seq.len, kStep), blocks = row_blocks<NR>(seq.n, in.g);
+  const long long unit = (cut - seq_first) / steps;
+  const long long first = seq_first + unit * steps, last = first + steps - 1;
+  if (first == cut) return;  // the cut lies between two units
+  const int p0 = (int)(first / line.piece), p1 = (int)(last / line.piece);  // pieces that hold the unit
+  const int nth = (int)blockIdx.x - p0, helpers = p1 - p0;
+  const int h = (int)(unit / blocks), rb = (int)(unit % blocks);
+  const int rows_here = min(kRows, seq.n * in.g - rb * kRows);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // piece p holds the unit as its first when the unit begins at or before the piece
+  auto part_of = [&](int p) -> const float* {
+    const int slot = 2 * p + (first <= line.piece * p ? 0 : 1);
+    return in.partial + (size_t)slot * partial_floats<D>(kRows);
+  };
+  const int group = threadIdx.x / 8, e = threadIdx.x % 8, lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  for (int item = nth; item < rows_here * (D / 32); item += helpers) {
+    const int row = item / (D / 32), d = 32 * (item % (D / 32)) + 4 * e;
+    float mm = -INFINITY;
+    for (int p = p0 + threadIdx.x; p <= p1; p += kThreads) mm = fmaxf(mm, part_of(p)[kRows * D + 2 * row]);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, off));
+    __syncthreads();
+    if (lane == 0) s_red[0][warp] = mm;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, s_red[0][w]);
+    float ll = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (mm != -INFINITY) {
+#pragma unroll 4
+      for (int p = p0 + group; p <= p1; p += kGroups) {
+        const float* part = part_of(p);
+        const float2 ml = *reinterpret_cast<const float2*>(part + kRows * D + 2 * row);
+        const float4 v = *reinterpret_cast<const float4*>(part + row * D + d);
+        const float f = ex2(ml.x - mm);
+        ll += ml.y * f;
+        o.x += v.x * f, o.y += v.y * f, o.z += v.z * f, o.w += v.w * f;
+      }
+    }
+    s_o[group][e] = o;
+    // every lane of a group holds the group's sum of weights; one of each group counts
+    float lw = e == 0 ? ll : 0.f;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) lw += __shfl_xor_sync(0xffffffffu, lw, off);
+    if (lane == 0) s_red[1][warp] = lw;
+    __syncthreads();
+    if (threadIdx.x < 8) {
+      float4 t = s_o[0][threadIdx.x];
+#pragma unroll
+      for (int i = 1; i < kGroups; ++i) {
+        const float4 v = s_o[i][threadIdx.x];
+        t.x += v.x, t.y += v.y, t.z += v.z, t.w += v.w;
+      }
+      float lt = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) lt += s_red[1][w];
+      const int at = rb * kRows + row;
+      const size_t out = (size_t)(seq.first + at / in.g) * in.heads + h * in.g + at % in.g;
+      const float inv = lt > 0.f ? 1.f / lt : 0.f;
+      *reinterpret_cast<uint2*>(in.o + out * D + d) =
+          make_uint2(pack_bf16(t.x * inv, t.y * inv), pack_bf16(t.z * inv, t.w * inv));
+      if (in.lse && d == 0) in.lse[out] = lt > 0.f ? (mm + log2f(lt)) * 0.69314718055994531f : -INFINITY;
+    }
+  }
+}
+
+template <int D, bool Q4, int NR>
+static int decode_impl(const CacheArgs& c, const AttnIn& in, cudaStream_t stream) {
+  s2_cache_decode_kernel<D, Q4, NR><<<kDecodePieces, kThreads, 0, stream>>>(c, in);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return (int)e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kDecodePieces - 1);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return (int)cudaLaunchKernelEx(&cfg, s2_cache_join_kernel<D, Q4, NR>, c, in);
+}
+
+template <int D, bool Q4>
+static int decode_rows(const CacheArgs& c, const AttnIn& in, int rows, cudaStream_t stream) {
+  return rows <= 8 ? decode_impl<D, Q4, 1>(c, in, stream) : decode_impl<D, Q4, 2>(c, in, stream);
+}
+
+int launch_cache_decode(const CacheArgs& c, const AttnIn& in, int D, bool q4, int rows, cudaStream_t stream) {
+  if (D == 64) return q4 ? decode_rows<64, true>(c, in, rows, stream) : decode_rows<64, false>(c, in, rows, stream);
+  return q4 ? decode_rows<128, true>(c, in, rows, stream) : decode_rows<128, false>(c, in, rows, stream);
+}
+
+size_t cache_decode_partial_bytes(int D) { return (size_t)2 * kDecodePieces * 16 * (D + 2) * sizeof(float); }
+
+}  // namespace s2

@@ -6,6 +6,9 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <cuda_bf16.h>
+
+#include "s2_cache.cuh"
 #include "s2_index.cuh"
 
 namespace s2 {
@@ -72,5 +75,39 @@ int launch_rope(const void* q, const void* k, void* q_out, void* k_out, const in
 
 // Per-position document bounds [B, N, 2] from per-position document IDs [B, N].
 int launch_doc_bounds(const int32_t* ids, int32_t* bounds, int B, int N, cudaStream_t stream);
+
+// Per-device set-up on first use (capability check): the status word's address, or an error code.
+int device_status(int** status);
+
+// Paged cache (s2_cache.cuh): new rows in, rows back out, attention over it.
+struct AppendIn {
+  const __nv_bfloat16* q;  // [T, q_heads, D], rows of a token ldq apart; null: q_heads = 0
+  const __nv_bfloat16* k;
+  const __nv_bfloat16* v;
+  __nv_bfloat16* q_out;  // [T, q_heads, D]
+  const int* positions;  // [T], or null: a token's place in its sequence
+  int64_t ldq, ldk, ldv;
+  int q_heads;
+  double turns[64];  // turns of pair j per position: scale·base^(-2j/D) / 2π
+};
+
+struct AttnIn {
+  const __nv_bfloat16* q;
+  __nv_bfloat16* o;  // [T, heads, D]
+  float* lse;        // [T, heads], or null
+  float* partial;    // workspace
+  int64_t ldq;
+  int heads, g;      // query heads, and query heads of a key/value head
+  float scale_log2;  // log2(e) / sqrt(D)
+  int pieces, min_piece;
+};
+
+constexpr int kDecodePieces = 592;  // CTAs of the decode kernel: 4 on each of 148 SMs
+
+int launch_cache_append(const CacheArgs& c, const AppendIn& in, int D, bool q4, bool rotate, cudaStream_t stream);
+int launch_cache_read(const CacheArgs& c, int D, bool q4, void* k_out, void* v_out, cudaStream_t stream);
+// rows: query rows of a unit at most, as far as the caller knows (a choice of tile only)
+int launch_cache_decode(const CacheArgs& c, const AttnIn& in, int D, bool q4, int rows, cudaStream_t stream);
+size_t cache_decode_partial_bytes(int D);
 
 }  // namespace s2

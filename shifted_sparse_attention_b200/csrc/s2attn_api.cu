@@ -173,6 +173,13 @@ unsigned long long current_context_id() {
   return id;
 }
 
+int device_status(int** status) {
+  DeviceState* st = nullptr;
+  const int rc = device_state(&st);
+  if (rc == S2_OK) *status = st->status;
+  return rc;
+}
+
 // Records a message for s2attn_last_error() from other translation units.
 int report_error(int code, const char* fmt, ...) {
   char buf[512];
@@ -574,6 +581,8 @@ int s2attn_check_status(void* stream) {
     return fail(S2_ERR_BOUNDS, "bounds check failed at site %d: value %lld outside [%lld, %lld) (flags 0x%x)",
                 area[2], r[0], r[1], r[2], flags);
   }
+  if (flags & s2::kCacheFlag)
+    return fail(S2_ERR_BOUNDS, "a page number, length or start of a cache batch is out of range (flags 0x%x)", flags);
   return fail(S2_ERR_TIMEOUT, "a kernel gave up waiting on a barrier (role flags 0x%x)", flags);
 }
 

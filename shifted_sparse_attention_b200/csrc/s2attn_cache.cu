@@ -1,0 +1,191 @@
+// s2attn_cache.cu -- the C ABI of the paged cache (include/s2attn.h): argument
+// checks, all before anything is enqueued, and launches.
+#include <cuda_runtime.h>
+
+#include <cmath>
+
+#include "../../include/s2attn.h"
+#include "s2_cache.cuh"
+#include "s2_kernels.h"
+
+namespace {
+
+using s2::report_error;
+
+bool aligned(const void* p, unsigned bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
+
+// Checks of the descriptors that every call shares; fills the kernels' view of them.
+int take(const s2_cache* cache, const s2_cache_batch* batch, s2::CacheArgs* a) {
+  if (!cache || !batch) return report_error(S2_ERR_INVALID_ARG, "null cache or batch descriptor");
+  if (cache->format != S2_CACHE_BF16 && cache->format != S2_CACHE_Q4)
+    return report_error(S2_ERR_INVALID_ARG, "unknown cache format %d", cache->format);
+  if (cache->pages < 1 || cache->heads < 1 || cache->page_size < 1 || cache->D < 1)
+    return report_error(S2_ERR_SHAPE, "pages, heads, page_size and D must be positive");
+  if (cache->D != 64 && cache->D != 128)
+    return report_error(S2_ERR_UNSUPPORTED, "D=%lld: the cache supports D in {64, 128}", (long long)cache->D);
+  const int64_t S = cache->page_size;
+  if (S != 16 && S != 32 && S != 64 && S != 128)
+    return report_error(S2_ERR_UNSUPPORTED, "page_size=%lld: pages hold 16, 32, 64 or 128 rows", (long long)S);
+  if (cache->heads > 65535 || cache->pages >= (int64_t(1) << 31) || cache->pages * cache->heads >= (int64_t(1) << 31))
+    return report_error(S2_ERR_UNSUPPORTED, "pages*heads must be below 2^31 and heads below 65536");
+  if (batch->seqs < 1 || batch->tokens < 1 || batch->table_width < 1)
+    return report_error(S2_ERR_SHAPE, "seqs, tokens and table_width must be positive");
+  if (batch->max_new < 0 || batch->max_new > batch->tokens)
+    return report_error(S2_ERR_SHAPE, "max_new=%lld must be in [0, tokens=%lld]", (long long)batch->max_new,
+                        (long long)batch->tokens);
+  if (batch->max_len < 0 || batch->table_width >= (int64_t(1) << 31) / S ||
+      batch->max_len > batch->table_width * S)
+    return report_error(S2_ERR_SHAPE, "max_len=%lld must be in [0, table_width*page_size], which is below 2^31",
+                        (long long)batch->max_len);
+  if (batch->seqs >= (int64_t(1) << 30) || batch->tokens >= (int64_t(1) << 30))
+    return report_error(S2_ERR_UNSUPPORTED, "seqs and tokens must be below 2^30");
+  if (!batch->q_starts && batch->tokens != batch->seqs)
+    return report_error(S2_ERR_SHAPE, "without q_starts each sequence has one new token (tokens=%lld, seqs=%lld)",
+                        (long long)batch->tokens, (long long)batch->seqs);
+  const bool q4 = cache->format == S2_CACHE_Q4;
+  if (!cache->k || !cache->v || (q4 && (!cache->k_scale || !cache->v_scale)) || !batch->page_table || !batch->seq_lens)
+    return report_error(S2_ERR_INVALID_ARG, "null pointer argument");
+  if (!q4 && (cache->k_scale || cache->v_scale))
+    return report_error(S2_ERR_INVALID_ARG, "a bf16 cache has no scales");
+  if (!aligned(cache->k, 16) || !aligned(cache->v, 16) || !aligned(cache->k_scale, 16) || !aligned(cache->v_scale, 16))
+    return report_error(S2_ERR_INVALID_ARG, "the cache's pointers must be 16-byte aligned");
+  if (!aligned(batch->page_table, 4) || !aligned(batch->seq_lens, 4) || !aligned(batch->q_starts, 4))
+    return report_error(S2_ERR_INVALID_ARG, "page_table, seq_lens and q_starts must be 4-byte aligned");
+  a->k = cache->k;
+  a->v = cache->v;
+  a->k_scale = cache->k_scale;
+  a->v_scale = cache->v_scale;
+  a->table = batch->page_table;
+  a->lens = batch->seq_lens;
+  a->starts = batch->q_starts;
+  a->pages = cache->pages;
+  a->heads = (int)cache->heads;
+  a->log2s = S == 16 ? 4 : S == 32 ? 5 : S == 64 ? 6 : 7;
+  a->B = (int)batch->seqs;
+  a->T = (int)batch->tokens;
+  a->width = (int)batch->table_width;
+  a->status = nullptr;
+  return S2_OK;
+}
+
+// Rows of a token that are `ld` elements apart hold heads*D elements and stay 16-byte aligned.
+int check_rows(const char* name, const void* p, int64_t ld, int64_t elements) {
+  if (!p) return report_error(S2_ERR_INVALID_ARG, "null pointer argument (%s)", name);
+  if (!aligned(p, 16)) return report_error(S2_ERR_INVALID_ARG, "%s must be 16-byte aligned", name);
+  if (ld < elements || ld % 8 || ld >= (int64_t(1) << 31))
+    return report_error(S2_ERR_SHAPE, "the row stride of %s (%lld) must be a multiple of 8 in [%lld, 2^31)", name,
+                        (long long)ld, (long long)elements);
+  return S2_OK;
+}
+
+// Query heads: a multiple of the key/value heads, at most 128 to one of them.
+int check_heads(const s2_cache* cache, int64_t heads) {
+  if (heads < 1 || heads % cache->heads)
+    return report_error(S2_ERR_SHAPE, "heads=%lld must be a positive multiple of the cache's %lld", (long long)heads,
+                        (long long)cache->heads);
+  if (heads / cache->heads > 128)
+    return report_error(S2_ERR_UNSUPPORTED, "%lld query heads to a key/value head: at most 128",
+                        (long long)(heads / cache->heads));
+  return S2_OK;
+}
+
+int launched(int rc, const char* what) {
+  if (rc == 0) return S2_OK;
+  return report_error(S2_ERR_CUDA, "%s launch failed: %s", what, cudaGetErrorString((cudaError_t)rc));
+}
+
+}  // namespace
+
+extern "C" {
+
+int s2attn_cache_append(const s2_cache* cache, const s2_cache_batch* batch, const void* q, int64_t ldq, const void* k,
+                        int64_t ldk, const void* v, int64_t ldv, void* q_out, int64_t heads, const int32_t* positions,
+                        double base, double scale, void* stream) {
+  s2::CacheArgs a;
+  int rc = take(cache, batch, &a);
+  if (rc) return rc;
+  const int64_t D = cache->D, kv = cache->heads * D;
+  if ((rc = check_rows("k", k, ldk, kv)) || (rc = check_rows("v", v, ldv, kv))) return rc;
+  const bool rotate = base != 0.0;
+  if (rotate && (!(base > 1.0) || !std::isfinite(base) || !(scale > 0.0) || !std::isfinite(scale)))
+    return report_error(S2_ERR_INVALID_ARG, "base must be 0 (no rotation) or finite and > 1, scale finite and > 0");
+  if (!q != !q_out) return report_error(S2_ERR_INVALID_ARG, "q and q_out go together");
+  if (q) {
+    if (!rotate) return report_error(S2_ERR_INVALID_ARG, "without a rotation (base 0) there is nothing to do with q");
+    if ((rc = check_heads(cache, heads)) || (rc = check_rows("q", q, ldq, heads * D)) ||
+        (rc = check_rows("q_out", q_out, heads * D, heads * D)))
+      return rc;
+  }
+  if (!aligned(positions, 4)) return report_error(S2_ERR_INVALID_ARG, "positions must be 4-byte aligned");
+  if ((rc = s2::device_status(&a.status))) return rc;
+  s2::AppendIn in;
+  in.q = static_cast<const __nv_bfloat16*>(q);
+  in.k = static_cast<const __nv_bfloat16*>(k);
+  in.v = static_cast<const __nv_bfloat16*>(v);
+  in.q_out = static_cast<__nv_bfloat16*>(q_out);
+  in.positions = positions;
+  in.ldq = ldq;
+  in.ldk = ldk;
+  in.ldv = ldv;
+  in.q_heads = q ? (int)heads : 0;
+  for (int j = 0; j < 64; ++j)
+    in.turns[j] = rotate && j < D / 2 ? scale * std::pow(base, -2.0 * j / (double)D) / 6.283185307179586477 : 0.0;
+  return launched(s2::launch_cache_append(a, in, (int)D, cache->format == S2_CACHE_Q4, rotate,
+                                          static_cast<cudaStream_t>(stream)),
+                  "cache append");
+}
+
+int s2attn_cache_read(const s2_cache* cache, const s2_cache_batch* batch, void* k_out, void* v_out, void* stream) {
+  s2::CacheArgs a;
+  int rc = take(cache, batch, &a);
+  if (rc) return rc;
+  const int64_t kv = cache->heads * cache->D;
+  if ((rc = check_rows("k_out", k_out, kv, kv)) || (rc = check_rows("v_out", v_out, kv, kv))) return rc;
+  if ((rc = s2::device_status(&a.status))) return rc;
+  return launched(s2::launch_cache_read(a, (int)cache->D, cache->format == S2_CACHE_Q4, k_out, v_out,
+                                        static_cast<cudaStream_t>(stream)),
+                  "cache read");
+}
+
+size_t s2attn_cache_attn_workspace_size(const s2_cache* cache, const s2_cache_batch* batch, int64_t heads) {
+  s2::CacheArgs a;
+  if (take(cache, batch, &a) != S2_OK || check_heads(cache, heads) != S2_OK) return 0;
+  return s2::cache_decode_partial_bytes((int)cache->D);
+}
+
+int s2attn_cache_attn(const s2_cache* cache, const s2_cache_batch* batch, const void* q, int64_t ldq, void* o,
+                      float* lse, int64_t heads, void* workspace, size_t workspace_bytes, void* stream) {
+  s2::CacheArgs a;
+  int rc = take(cache, batch, &a);
+  if (rc) return rc;
+  if ((rc = check_heads(cache, heads))) return rc;
+  const int64_t D = cache->D;
+  if ((rc = check_rows("q", q, ldq, heads * D)) || (rc = check_rows("o", o, heads * D, heads * D))) return rc;
+  if (heads * batch->tokens >= (int64_t(1) << 31))
+    return report_error(S2_ERR_UNSUPPORTED, "tokens*heads must be below 2^31");
+  if (!aligned(lse, 4)) return report_error(S2_ERR_INVALID_ARG, "lse must be 4-byte aligned");
+  if (!workspace || !aligned(workspace, 256))
+    return report_error(S2_ERR_INVALID_ARG, "workspace must be given and 256-byte aligned");
+  const size_t need = s2attn_cache_attn_workspace_size(cache, batch, heads);
+  if (workspace_bytes < need)
+    return report_error(S2_ERR_INVALID_ARG, "workspace of %zu bytes is smaller than the %zu needed", workspace_bytes,
+                        need);
+  if ((rc = s2::device_status(&a.status))) return rc;
+  s2::AttnIn in;
+  in.q = static_cast<const __nv_bfloat16*>(q);
+  in.o = static_cast<__nv_bfloat16*>(o);
+  in.lse = lse;
+  in.partial = static_cast<float*>(workspace);
+  in.ldq = ldq;
+  in.heads = (int)heads;
+  in.g = (int)(heads / cache->heads);
+  in.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)D));
+  in.pieces = s2::kDecodePieces;
+  in.min_piece = 16;
+  const int64_t rows = (batch->max_new ? batch->max_new : batch->tokens) * in.g;
+  return launched(s2::launch_cache_decode(a, in, (int)D, cache->format == S2_CACHE_Q4, rows > 16 ? 16 : (int)rows,
+                                          static_cast<cudaStream_t>(stream)),
+                  "cache attention");
+}
+
+}  // extern "C"

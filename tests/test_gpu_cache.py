@@ -1,0 +1,394 @@
+"""The paged cache of keys and values on the GPU (needs a B200): append, read and attention against the 64-bit
+reference (tests/cache_ref.py), which also derives the tolerances."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+import shifted_sparse_attention_b200 as s2
+from tests import cache_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+
+def starts_of(news):
+    return torch.tensor([0] + list(news)).cumsum(0).to(torch.int32)
+
+
+def on_gpu(c):
+    return s2.KVCache(*[t.cuda() for t in (c.k, c.v, c.ks, c.vs) if t is not None])
+
+
+def batch_of(c, news, plain=False, extra=0, **hints):
+    lens = torch.tensor(c.lens, dtype=torch.int32).cuda()
+    starts = None if plain else starts_of(news).cuda()
+    return s2.CacheBatch(c.table.cuda(), lens, starts, sum(news) + extra, **hints)
+
+
+def check_attention(c, news, H, seed=0, plain=False, **hints):
+    T = sum(news)
+    g = torch.Generator().manual_seed(seed)
+    q = torch.randn(T, H, c.dim, generator=g).bfloat16()
+    o, lse, to, tl = ref.attention(c, q, starts_of(news))
+    got_lse = torch.empty(T, H, device="cuda")
+    got = s2.cache_attention(on_gpu(c), batch_of(c, news, plain, **hints), q.cuda(), lse=got_lse)
+    s2.check_status()
+    got, got_lse = got.double().cpu(), got_lse.double().cpu()
+    assert torch.isfinite(got).all()
+    over = (got - o).abs() - to
+    assert (over <= 0).all(), ("o", float(over.max()), int((over > 0).sum()))
+    empty = lse.isinf()
+    assert torch.equal(got_lse.isinf(), empty)
+    off = ((got_lse - lse).abs() - tl)[~empty]
+    assert off.numel() == 0 or (off <= 0).all(), ("lse", float(off.max()))
+    return got
+
+
+STEPS = [  # (lens, new tokens)
+    ([1], [1]),
+    ([15], [1]),
+    ([16], [1]),
+    ([17], [1]),
+    ([513], [1]),
+    ([128, 129, 1, 127, 64], [1] * 5),
+    ([20000], [1]),
+    ([5000, 3, 9001, 700], [1, 1, 2, 3]),
+]
+
+
+@pytest.mark.parametrize("bits", [16, 4])
+@pytest.mark.parametrize("D,H,Hkv,S", [(128, 8, 2, 16), (64, 3, 3, 64)])
+@pytest.mark.parametrize("lens,news", STEPS)
+def test_few_new_tokens(bits, D, H, Hkv, S, lens, news):
+    c = ref.Paged(lens, Hkv, D, S, bits, seed=len(lens) + lens[0])
+    check_attention(c, news, H, plain=all(n == 1 for n in news), max_new=max(news))
+
+
+@pytest.mark.parametrize("bits", [16, 4])
+@pytest.mark.parametrize("D", [128, 64])
+@pytest.mark.parametrize("H,Hkv", [(7, 1), (16, 1), (17, 1), (40, 2), (12, 4)])
+def test_heads_shared_by_key_heads(bits, D, H, Hkv):
+    c = ref.Paged([700, 31], Hkv, D, 32, bits, seed=H)
+    check_attention(c, [1, 1], H, max_new=1)
+    check_attention(c, [3, 2], H, max_new=3)
+
+
+@pytest.mark.parametrize("bits", [16, 4])
+@pytest.mark.parametrize("D,H,Hkv,S", [(128, 4, 2, 128), (64, 6, 2, 16), (128, 5, 1, 64)])
+@pytest.mark.parametrize("lens,news", [
+    ([200], [200]),                 # a whole prompt: the first token sees one key
+    ([129, 1000], [129, 130]),
+    ([640, 64, 1], [256, 64, 1]),   # chunks beside a single token
+    ([1200], [700]),
+])
+def test_chunks_of_prompts(bits, D, H, Hkv, S, lens, news):
+    c = ref.Paged(lens, Hkv, D, S, bits, seed=lens[0])
+    check_attention(c, news, H, max_new=max(news), max_len=max(lens))
+
+
+@pytest.mark.parametrize("bits", [16, 4])
+@pytest.mark.parametrize("max_new", [1, 0])
+def test_rows_that_see_nothing_and_sequences_left_out(bits, max_new):
+    # lengths of zero (a padded batch), fewer rows than new tokens, no new token
+    lens, news = [0, 40, 2, 300, 0], [1, 1, 5, 0, 3]
+    c = ref.Paged(lens, 2, 128, 16, bits)
+    got = check_attention(c, news, 4, max_new=max_new)
+    assert (got[0] == 0).all() and (got[2:5] == 0).all() and (got[5] != 0).any()
+
+
+@pytest.mark.parametrize("max_new", [1, 200])
+def test_hints_change_no_result_and_runs_repeat_bitwise(max_new):
+    lens, news = [1500, 260, 77], [1, 200, 3]
+    c = ref.Paged(lens, 2, 128, 64, 16)
+    a = check_attention(c, news, 8, max_new=max_new)
+    b = check_attention(c, news, 8, max_new=max_new, max_len=1500)
+    assert torch.equal(a, check_attention(c, news, 8, max_new=max_new)) and (a - b).abs().max() < 2e-2
+
+
+@pytest.mark.parametrize("bits", [16, 4])
+def test_tokens_of_no_sequence_are_left_as_they_were(bits):
+    c = ref.Paged([90, 33], 2, 64, 16, bits)
+    news, extra, before = [2, 1], 4, 3
+    T = sum(news) + extra + before
+    starts = (starts_of(news) + before).to(torch.int32).cuda()
+    batch = s2.CacheBatch(c.table.cuda(), torch.tensor(c.lens, dtype=torch.int32).cuda(), starts, T, max_new=2)
+    q = torch.randn(T, 4, 64).bfloat16().cuda()
+    out, lse = torch.full((T, 4, 64), 7.0).bfloat16().cuda(), torch.full((T, 4), 7.0).cuda()
+    s2.cache_attention(on_gpu(c), batch, q, out=out, lse=lse)
+    rows = [torch.full((T, 2, 64), 7.0).bfloat16().cuda() for _ in range(2)]
+    s2.cache_read(on_gpu(c), batch, out=rows)
+    cache = on_gpu(c)
+    rq = torch.full_like(q, 7.0)
+    s2.cache_append(cache, batch, *[torch.randn(T, 2, 64).bfloat16().cuda() for _ in range(2)], q, out=rq)
+    s2.check_status()
+    for t in (out, lse, *rows, rq):
+        assert (t[:before] == 7).all() and (t[before + sum(news):] == 7).all()
+        assert (t[before:before + sum(news)] != 7).any()
+
+
+def test_extreme_scores():
+    # a key so large that one weight is all, or none
+    c = ref.Paged([64], 1, 128, 16, 16)
+    c.k[c.table[0, 1].long(), 0, 3] *= 100
+    for seed in range(4):
+        check_attention(c, [1], 1, seed=seed, plain=True)
+
+
+def test_infinite_value_in_a_visible_row():
+    # an infinite value reaches its channel and no other (its weight is far from 0 here)
+    c = ref.Paged([64], 1, 128, 16, 16)
+    cache, batch = on_gpu(c), batch_of(c, [1], plain=True)
+    cache.v[c.table[0, 3].long(), 0, 15, 5] = float("inf")
+    q = 0.1 * torch.randn(1, 1, 128, generator=torch.Generator().manual_seed(0))
+    got = s2.cache_attention(cache, batch, q.bfloat16().cuda())
+    assert torch.isinf(got[0, 0, 5]) and torch.isfinite(got[0, 0, :5]).all() and torch.isfinite(got[0, 0, 6:]).all()
+
+
+def test_strided_queries():
+    c = ref.Paged([77, 400], 2, 128, 32, 16)
+    wide = torch.randn(2, 8 * 128 + 64).bfloat16()
+    q = wide[:, 64:].unflatten(1, (8, 128))
+    batch = batch_of(c, [1, 1], plain=True)
+    a = s2.cache_attention(on_gpu(c), batch, wide.cuda()[:, 64:].unflatten(1, (8, 128)))
+    b = s2.cache_attention(on_gpu(c), batch, q.contiguous().cuda())
+    assert torch.equal(a, b)
+
+
+def test_rows_beyond_32_bit_offsets():
+    # 2^18 pages of 64 rows of 128 channels x 2 heads in bf16: 4.3e9 elements a tensor (8.6 GB); the sequence lives at
+    # its end
+    pages, S, Hkv, D = (1 << 18) + 8, 64, 2, 128
+    cache = s2.KVCache.empty(pages, S, Hkv, D)
+    c = ref.Paged([150, 64], Hkv, D, S, 16, spare=0)
+    shift = pages - c.k.shape[0]
+    cache.k[shift:], cache.v[shift:] = c.k.cuda(), c.v.cuda()
+    table = torch.where(c.table >= 0, c.table + shift, c.table).cuda()
+    lens = torch.tensor(c.lens, dtype=torch.int32).cuda()
+    for news in ([1, 1], [150, 64]):
+        starts = starts_of(news)
+        q = torch.randn(sum(news), 4, D).bfloat16()
+        o, _, to, _ = ref.attention(c, q, starts)
+        batch = s2.CacheBatch(table, lens, starts.cuda(), sum(news), max_new=max(news))
+        got = s2.cache_attention(cache, batch, q.cuda())
+        assert ((got.double().cpu() - o).abs() <= to).all()
+    k, _ = s2.cache_read(cache, batch)
+    assert torch.equal(k[:150, 1].cpu().double(), c.rows(0, 1)[0])
+    s2.check_status()
+
+
+# ---------------------------------------------------------------- append and read
+
+
+def check_append(lens, news, H, Hkv, D, S, bits, base=10000.0, scale=1.0, positions=None, seed=0):
+    c = ref.Paged(lens, Hkv, D, S, bits, seed=seed)
+    T = sum(news)
+    g = torch.Generator().manual_seed(seed + 1)
+    qkv = torch.randn(T, (H + 2 * Hkv) * D, generator=g).bfloat16()
+    q, k, v = qkv.split([H * D, Hkv * D, Hkv * D], 1)
+    q, k, v = q.unflatten(1, (H, D)), k.unflatten(1, (Hkv, D)), v.unflatten(1, (Hkv, D))
+    place = torch.cat([n - m + torch.arange(m) for n, m in zip(lens, news)])
+    pos = place if positions is None else positions
+    cache, batch = on_gpu(c), batch_of(c, news)
+    before = [t.clone() for t in (cache.k, cache.v)]
+    dev = qkv.cuda()
+    dq, dk, dv = (t.unflatten(1, (-1, D)) for t in dev.split([H * D, Hkv * D, Hkv * D], 1))
+    kw = {} if positions is None else {"positions": positions.to(torch.int32).cuda()}
+    out = s2.cache_append(cache, batch, dk, dv, dq if base else None, base=base, scale=scale, **kw)
+    rk, rv = s2.cache_read(cache, batch)
+    s2.check_status()
+    stored = place >= 0
+
+    def near(got, want, pair):
+        # the rotation: sine and cosine to 3e-7 (angle in turns rounded to 32 bits), two products and a sum, a rounding
+        slack = 6e-7 * pair + 2.0 ** -23 * want.abs()
+        assert ((got - want).abs() <= ref.U * (want.abs() + slack) + slack).all()
+
+    def pair_size(x):
+        h = D // 2
+        s = x.double()[..., :h].abs() + x.double()[..., h:].abs()
+        return torch.cat([s, s], -1)
+
+    kr = ref.rotate(k, pos, base, scale) if base else k.double()
+    if base:
+        near(out.double().cpu(), ref.rotate(q, pos, base, scale), pair_size(q))
+    else:
+        assert out is None
+    gk, gv = rk.double().cpu()[stored], rv.double().cpu()[stored]
+    if bits == 16:
+        near(gk, kr[stored], pair_size(k)[stored]) if base else None
+        assert base or torch.equal(gk, kr[stored])
+        assert torch.equal(gv, v.double()[stored])
+    else:
+        # values: exactly what the definition makes of them
+        cv, sv, mv = ref.pack(v[stored])
+        assert torch.equal(gv, (mv[..., None] + sv[..., None] * cv).float().bfloat16().double())
+        # keys: the rotated row may differ from the reference's by a step of bf16, so a code by one
+        ck, sk, mk = ref.pack(kr[stored].bfloat16())
+        want = mk[..., None] + sk[..., None] * ck
+        assert ((gk - want).abs() <= 1.1 * sk[..., None] + 2 * ref.U * want.abs()).all()
+        assert ((gk - want).abs() > ref.U * want.abs() + 2.0 ** -7 * sk[..., None] + 1e-6).double().mean() < 1e-3
+        # half a step of the grid, the scale's rounding, and the row's own roundings to bf16
+        size = kr[stored].abs().amax(-1, keepdim=True)
+        assert ((gk - kr[stored]).abs() <= 0.55 * sk[..., None] + 3 * ref.U * size).all()
+    # nothing else was written
+    touched = torch.zeros(c.k.shape[:3], dtype=torch.bool)
+    at = 0
+    for b, (n, m) in enumerate(zip(lens, news)):
+        for i in range(m):
+            p = n - m + i
+            if p >= 0:
+                touched[int(c.table[b, p // S]), :, p % S] = True
+        at += m
+    for t, old in zip((cache.k, cache.v), before):
+        a, o = t.cpu()[~touched], old.cpu()[~touched]
+        assert torch.equal(a.view(torch.uint8), o.view(torch.uint8))
+    return cache, batch
+
+
+@pytest.mark.parametrize("bits", [16, 4])
+@pytest.mark.parametrize("D,H,Hkv,S", [(128, 4, 2, 16), (64, 5, 5, 128), (128, 9, 1, 64)])
+@pytest.mark.parametrize("lens,news", [
+    ([1], [1]), ([257], [1]), ([130, 1, 64], [130, 1, 33]), ([900, 17, 0, 3], [2, 17, 1, 0]), ([5, 40], [9, 1]),
+])
+def test_append_and_read(bits, D, H, Hkv, S, lens, news):
+    check_append(lens, news, H, Hkv, D, S, bits, seed=lens[0])
+
+
+@pytest.mark.parametrize("bits", [16, 4])
+def test_append_at_given_positions_and_unrotated(bits):
+    pos = torch.tensor([0, 1, 8191, 99999, 1000000, 2 ** 31 - 1, 7])
+    check_append([40, 9], [4, 3], 4, 2, 128, 32, bits, base=500000.0, scale=0.25, positions=pos)
+    check_append([40, 9], [4, 3], 4, 2, 64, 32, bits, base=0.0)
+
+
+def test_packing_of_flat_and_broken_rows():
+    cache = s2.KVCache.empty(1, 16, 1, 64, bits=4)
+    lens = torch.tensor([4], dtype=torch.int32).cuda()
+    batch = s2.CacheBatch(torch.zeros(1, 1, dtype=torch.int32).cuda(), lens,
+                          torch.tensor([0, 4], dtype=torch.int32).cuda(), 4)
+    x = torch.randn(4, 1, 64).bfloat16()
+    x[0] = -3.0                       # all equal: scale 0
+    x[1, 0, 5] = float("nan")
+    x[2, 0, 63] = float("inf")
+    s2.cache_append(cache, batch, x.cuda(), x.cuda(), base=0.0)
+    k, v = s2.cache_read(cache, batch)
+    for t in (k, v):
+        assert (t[0] == -3.0).all() and torch.isnan(t[1:3]).all() and torch.isfinite(t[3]).all()
+
+
+def test_numbers_out_of_range_are_reported_and_touch_nothing():
+    c = ref.Paged([40, 33], 2, 64, 16, 16)
+    T = 2
+
+    def batch(**kw):
+        a = dict(page_table=c.table.clone(), seq_lens=torch.tensor([40, 33], dtype=torch.int32),
+                 q_starts=torch.tensor([0, 1, 2], dtype=torch.int32))
+        for name, (at, value) in kw.items():
+            a[name][at] = value
+        return s2.CacheBatch(*[t.cuda() for t in a.values()], T)
+
+    x = torch.randn(T, 2, 64).bfloat16().cuda()
+    good = s2.cache_attention(on_gpu(c), batch(), x)
+    s2.check_status()
+    for kw in (dict(page_table=((0, 2), 10 ** 6)), dict(page_table=((0, 2), -1)), dict(seq_lens=(0, 10 ** 6)),
+               dict(seq_lens=(0, -3)), dict(q_starts=(0, 2)), dict(q_starts=(0, -1))):
+        cache = on_gpu(c)
+        got = s2.cache_attention(cache, batch(**kw), x)
+        with pytest.raises(s2.S2AttnError) as e:
+            s2.check_status()
+        assert e.value.code == -6
+        assert torch.equal(got[1], good[1])  # the other sequence is served
+        s2.cache_append(cache, batch(**kw), x, x, base=0.0)
+        with pytest.raises(s2.S2AttnError):
+            s2.check_status()
+        at = c.table[0, 2].long()
+        assert torch.equal(cache.k[at].cpu().view(torch.int16), c.k[at].view(torch.int16))
+    s2.check_status()
+
+
+# ---------------------------------------------------------------- a serving program
+
+
+@pytest.mark.parametrize("bits", [16, 4])
+def test_prompt_in_chunks_and_steps_match_the_dense_forward(bits):
+    """A prompt appended in two chunks, then single steps, against the framework's dense-causal forward over the keys
+    and values that the cache holds."""
+    N, H, Hkv, D, S = 640, 8, 2, 128, 64
+    g = torch.Generator().manual_seed(5)
+    q, k, v = (torch.randn(N, h, D, generator=g).bfloat16().cuda() for h in (H, Hkv, Hkv))
+    cache = s2.KVCache.empty(12, S, Hkv, D, bits=bits)
+    table = torch.randperm(12, generator=g)[: N // S].to(torch.int32)[None].cuda()
+    lens = torch.zeros(1, dtype=torch.int32).cuda()
+    outs, rq = [], []
+    at = 0
+    for n in (300, 329) + (1,) * 11:
+        lens += n
+        batch = s2.CacheBatch(table, lens, torch.tensor([0, n], dtype=torch.int32).cuda(), n, max_new=n)
+        r = s2.cache_append(cache, batch, k[at:at + n], v[at:at + n], q[at:at + n])
+        outs.append(s2.cache_attention(cache, batch, r))
+        rq.append(r)
+        at += n
+    whole = s2.CacheBatch(table, lens, torch.tensor([0, N], dtype=torch.int32).cuda(), N)
+    ck, cv = s2.cache_read(cache, whole)
+    s2.check_status()
+    fk, fv = (t.repeat_interleave(H // Hkv, 1)[None].contiguous() for t in (ck, cv))
+    o, _ = s2.forward(torch.cat(rq)[None].contiguous(), fk, fv, N, s2.DENSE_CAUSAL)
+    got = torch.cat(outs).double()
+    # both sides round weights and results (4 U), and the read-back rows of 4 bits once more (2 U)
+    off = (got - o[0].double()).abs()
+    assert (off <= 6 * ref.U * (fv[0].abs().double().amax())).all() and off.mean() < 2e-3
+
+
+@pytest.mark.parametrize("bits", [16, 4])
+def test_steps_captured_in_a_graph(bits):
+    """One captured step, replayed while the program moves lengths and tokens on, against eager calls."""
+    Hkv, H, D, S = 2, 8, 128, 16
+    lens0 = [5, 130, 47]
+    c = ref.Paged([n + 40 for n in lens0], Hkv, D, S, bits, fill=0.0)
+    cache, twin = on_gpu(c), on_gpu(c)
+    lens = torch.tensor(lens0, dtype=torch.int32).cuda()
+    batch = s2.CacheBatch(c.table.cuda(), lens, max_len=170)
+    q, k, v = (torch.zeros(3, h, D, dtype=torch.bfloat16, device="cuda") for h in (H, Hkv, Hkv))
+    rq, o = torch.empty_like(q), torch.empty_like(q)
+    ws = s2.cache_attention_workspace(cache, batch, H)
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        s2.cache_append(cache, batch, k, v, q, out=rq)
+        s2.cache_attention(cache, batch, rq, out=o, workspace=ws)
+    torch.cuda.current_stream().wait_stream(side)
+    with torch.cuda.graph(graph):
+        s2.cache_append(cache, batch, k, v, q, out=rq)
+        s2.cache_attention(cache, batch, rq, out=o, workspace=ws)
+    cache.k.copy_(c.k), cache.v.copy_(c.v)
+    if bits == 4:
+        cache.k_scale.copy_(c.ks), cache.v_scale.copy_(c.vs)
+    g = torch.Generator().manual_seed(1)
+    for _ in range(35):
+        for t in (q, k, v):
+            t.copy_(torch.randn(t.shape, generator=g))
+        lens += 1
+        graph.replay()
+        want = s2.cache_attention(twin, batch, s2.cache_append(twin, batch, k, v, q))
+        assert torch.equal(o, want)
+    assert torch.equal(cache.k.view(torch.uint8), twin.k.view(torch.uint8))
+    s2.check_status()
+
+
+def test_calls_on_other_streams():
+    """Calls given a stream allocate on it and run there, two at once with a workspace each."""
+    c = ref.Paged([3000, 200], 2, 128, 64, 16)
+    cache, batch = on_gpu(c), batch_of(c, [1, 1], plain=True)
+    q = torch.randn(2, 8, 128).bfloat16().cuda()
+    want = s2.cache_attention(cache, batch, q)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(20):
+        for s in streams:
+            outs.append(s2.cache_attention(cache, batch, q, stream=s))
+        outs.append(s2.cache_attention(cache, batch, q, stream=streams[0].cuda_stream))
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for o in outs)
+    s2.check_status()
