@@ -79,4 +79,84 @@ __device__ __forceinline__ float2 q4_pair(uint32_t raw) {
   return make_float2(__uint_as_float(raw << 16), __uint_as_float(raw & 0xffff0000u));
 }
 
+// ---------------------------------------------------------------- cutting the work into equal pieces
+// All sequences' work, weighed by `weight(b)`, forms one line that is cut into
+// equal pieces, one per CTA.  The lengths are only known on the device, so
+// every CTA adds the weights up by itself: they are a few KB, and in L2.
+struct Line {
+  long long total, piece;
+};
+
+// Shared memory of the two calls below: kThreads / 32 + 2 values.
+template <int kThreads, typename Weight>
+__device__ __forceinline__ Line make_line(int B, int pieces, long long min_piece, long long* sh, Weight weight) {
+  constexpr int kW = kThreads / 32;
+  long long v = 0;
+  for (int b = threadIdx.x; b < B; b += kThreads) v += weight(b);
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+  __syncthreads();
+  if (threadIdx.x % 32 == 0) sh[threadIdx.x / 32] = v;
+  __syncthreads();
+  Line l;
+  l.total = 0;
+#pragma unroll
+  for (int w = 0; w < kW; ++w) l.total += sh[w];
+  l.piece = (l.total + pieces - 1) / pieces;
+  if (l.piece < min_piece) l.piece = min_piece;
+  return l;
+}
+
+// Sequence that holds point x of the line, and the point where it begins.  All threads get both.
+template <int kThreads, typename Weight>
+__device__ __forceinline__ void find_seq(int B, long long x, long long* sh, Weight weight, int& b_out,
+                                         long long& first_out) {
+  constexpr int kW = kThreads / 32;
+  long long before = 0;
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  for (int b0 = 0; b0 < B; b0 += kThreads) {
+    const int b = b0 + threadIdx.x;
+    const long long mine = b < B ? weight(b) : 0;
+    long long upto = mine;  // inclusive sum over the warp
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, upto, off);
+      if (lane >= off) upto += y;
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) sh[kW] = -1;
+    if (lane == 31) sh[warp] = upto;
+    __syncthreads();
+    long long base = before, all = 0;
+#pragma unroll
+    for (int w = 0; w < kW; ++w) {
+      if (w < warp) base += sh[w];
+      all += sh[w];
+    }
+    const long long end = base + upto;
+    if (x < end && x >= end - mine) {
+      sh[kW] = b;
+      sh[kW + 1] = end - mine;
+    }
+    __syncthreads();
+    if (sh[kW] >= 0) {
+      b_out = (int)sh[kW];
+      first_out = sh[kW + 1];
+      return;
+    }
+    before += all;
+  }
+  b_out = -1;
+  first_out = 0;
+}
+
+// ---------------------------------------------------------------- 4-bit codes as bf16
+// Two codes (bits [0,4) and [16,20) of x) as bf16 code - 8: 0x4300 | c is 128 + c.
+__device__ __forceinline__ uint32_t less_136(uint32_t y) {
+  const __nv_bfloat162 off = __halves2bfloat162(__ushort_as_bfloat16(0x4308), __ushort_as_bfloat16(0x4308));
+  const __nv_bfloat162 z = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&y), off);
+  return *reinterpret_cast<const uint32_t*>(&z);
+}
+__device__ __forceinline__ uint32_t codes_bf16(uint32_t x) { return less_136((x & 0x000f000fu) | 0x43004300u); }
+
 }  // namespace s2

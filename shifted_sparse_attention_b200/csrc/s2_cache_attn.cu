@@ -58,14 +58,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   return y;
 }
 
-// Two codes (bits [0,4) and [16,20) of x) as bf16 code - 8: 0x4300 | c is 128 + c.
-__device__ __forceinline__ uint32_t codes_bf16(uint32_t x) {
-  const uint32_t y = (x & 0x000f000fu) | 0x43004300u;
-  const __nv_bfloat162 off = __halves2bfloat162(__ushort_as_bfloat16(0x4308), __ushort_as_bfloat16(0x4308));
-  const __nv_bfloat162 z = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&y), off);
-  return *reinterpret_cast<const uint32_t*>(&z);
-}
-
 // The caches are read once: past L1, and first to leave L2.
 __device__ __forceinline__ uint4 ld_stream16(const void* p) {
   uint4 v;
@@ -174,81 +166,11 @@ __device__ __forceinline__ int row_blocks(int n, int g) {
   return (int)(((long long)n * g + 8 * NR - 1) / (8 * NR));
 }
 
-// Where the line of all steps is cut, and the sequence that holds a given step of it.
-struct Line {
-  long long total, piece;
-};
-
-// Sum over the CTA's threads; all threads get it.
-__device__ __forceinline__ long long cta_sum(long long v, long long* sh) {
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-  __syncthreads();
-  if (threadIdx.x % 32 == 0) sh[threadIdx.x / 32] = v;
-  __syncthreads();
-  long long s = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) s += sh[w];
-  return s;
-}
-
+// Steps of sequence b on the line.
 template <int NR>
 __device__ __forceinline__ long long seq_steps(const CacheArgs& c, const AttnIn& in, int b, int step) {
   const Seq s = load_seq(c, b);
   return (long long)c.heads * row_blocks<NR>(s.n, in.g) * steps_of(s.len, step);
-}
-
-template <int NR>
-__device__ __forceinline__ Line make_line(const CacheArgs& c, const AttnIn& in, int step, long long* sh) {
-  long long mine = 0;
-  for (int b = threadIdx.x; b < c.B; b += kThreads) mine += seq_steps<NR>(c, in, b, step);
-  Line l;
-  l.total = cta_sum(mine, sh);
-  l.piece = (l.total + in.pieces - 1) / in.pieces;
-  if (l.piece < in.min_piece) l.piece = in.min_piece;
-  return l;
-}
-
-// Sequence that holds step x of the line, and the line's first step of it (all threads; sh: kWarps + 2 values).
-template <int NR>
-__device__ __forceinline__ void find_seq(const CacheArgs& c, const AttnIn& in, int step, long long x, long long* sh,
-                                         int& b_out, long long& first_out) {
-  long long before = 0;
-  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  for (int b0 = 0; b0 < c.B; b0 += kThreads) {
-    const int b = b0 + threadIdx.x;
-    const long long mine = b < c.B ? seq_steps<NR>(c, in, b, step) : 0;
-    long long upto = mine;  // inclusive sum over the warp
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, upto, off);
-      if (lane >= off) upto += y;
-    }
-    __syncthreads();
-    if (threadIdx.x == 0) sh[kWarps] = -1;
-    if (lane == 31) sh[warp] = upto;
-    __syncthreads();
-    long long base = before, all = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) base += sh[w];
-      all += sh[w];
-    }
-    const long long end = base + upto;
-    if (x < end && x >= end - mine) {
-      sh[kWarps] = b;
-      sh[kWarps + 1] = end - mine;
-    }
-    __syncthreads();
-    if (sh[kWarps] >= 0) {
-      b_out = (int)sh[kWarps];
-      first_out = sh[kWarps + 1];
-      return;
-    }
-    before += all;
-  }
-  b_out = -1;
-  first_out = 0;
 }
 
 }  // namespace
@@ -272,13 +194,14 @@ __global__ void __launch_bounds__(kThreads, NR == 1 ? 4 : 2)
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, r = lane / 4, cc = lane % 4;
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join may start its own set-up
-  const Line line = make_line<NR>(c, in, kStep, sh);
+  auto weight = [&](int i) { return seq_steps<NR>(c, in, i, kStep); };
+  const Line line = make_line<kThreads>(c.B, in.pieces, in.min_piece, sh, weight);
   const long long x0 = line.piece * blockIdx.x;
   if (x0 >= line.total) return;
   const long long x1 = min(x0 + line.piece, line.total);
   int b;
   long long seq_first;
-  find_seq<NR>(c, in, kStep, x0, sh, b, seq_first);
+  find_seq<kThreads>(c.B, x0, sh, weight, b, seq_first);
 
   long long x = x0;
   while (x < x1) {
@@ -629,12 +552,13 @@ __global__ void __launch_bounds__(kThreads) s2_cache_join_kernel(const __grid_co
   __shared__ long long sh[kWarps + 2];
   __shared__ float s_red[2][kWarps];
   __shared__ float4 s_o[kGroups][8];
-  const Line line = make_line<NR>(c, in, kStep, sh);
+  auto weight = [&](int i) { return seq_steps<NR>(c, in, i, kStep); };
+  const Line line = make_line<kThreads>(c.B, in.pieces, in.min_piece, sh, weight);
   const long long cut = line.piece * (blockIdx.x + 1);
   if (cut >= line.total) return;
   int b;
   long long seq_first;
-  find_seq<NR>(c, in, kStep, cut, sh, b, seq_first);
+  find_seq<kThreads>(c.B, cut, sh, weight, b, seq_first);
   const Seq seq = load_seq(c, b);
   const int steps = steps_of(seq.len, kStep), blocks = row_blocks<NR>(seq.n, in.g);
   const long long unit = (cut - seq_first) / steps;

@@ -1,0 +1,859 @@
+// s2_cache_chunk.cu -- attention of many new tokens over a paged cache
+// (chunks of prompts): the operator of s2_cache_attn.cu where the products
+// bound it, on the tensor cores (tcgen05, TMEM), fed by TMA.
+//
+// Rows: the g query heads of a key/value head share its keys, so a tile of
+// query rows is (128 / g tokens) x (g heads), 128 rows for g a power of two, and
+// a unit is two such tiles (A, B: consecutive tokens) of one key/value head.
+// Its keys go by in tiles of 128: 128 / S pages, each brought by TMA into its
+// rows of the tile (or, in 4 bits, unpacked there by a warpgroup).
+//
+// Work: the units' keys form one line (s2_cache.cuh) cut into one piece per
+// SM, so a few long units load all SMs as well as many short ones.  CTAs stay
+// for their whole piece: tensor memory, barriers and the load pipeline run on
+// from unit to unit, so a unit's epilogue overlaps the next one's first
+// products.  A unit cut by a border leaves partial sums for
+// s2_cache_chunk_join.
+//
+// Warp roles: warps 0-3 softmax of tile A (thread = query row = TMEM lane),
+// 4-7 of tile B, 8 TMA, 9 MMA issue; with 4-bit pages warps 10 and 11 unpack
+// (with or without them the softmax warps have 168 registers).  MMA order, TMEM layout and
+// the softmax are those of s2_fwd.cu: S and P share columns, P feeds O += P V
+// from TMEM, and the running maximum moves in steps of 8 (in powers of two).
+//
+// 4 bits: tiles hold codes - 8 (whole numbers, exact in bf16).  The softmax
+// applies scale and min of each key: s = sk (q·c') + (mk + 8 sk) sum(q); the
+// weight that goes into the product is p·sv (rounded to bf16, relative 2^-9),
+// and sum p (mv + 8 sv), the same for every channel, is kept beside O.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "s2_cache.cuh"
+#include "s2_kernels.h"
+#include "sm100_ptx.cuh"
+
+namespace s2 {
+
+namespace chunk {
+
+constexpr int kT = 128;  // rows of a tile, of queries and of keys
+constexpr int kChunkBytes = kT * 128;
+constexpr int kSegs = 48;          // units (or parts) that a CTA looks ahead
+constexpr int kScaleSlots = 4;
+constexpr long long kUnitKeys = 256;  // what starting and ending a unit costs, in keys
+
+template <bool Q4>
+__host__ __device__ constexpr int threads() { return Q4 ? 384 : 320; }
+template <bool Q4>
+__host__ __device__ constexpr int slots() { return Q4 ? 4 : 5; }
+
+enum Bar {
+  KV_FULL = 0,                          // + slot (5)
+  KV_EMPTY = 5,                         // + slot (5)
+  S_FULL = 10,                          // + tile (2)
+  P_FULL = 12,                          // + tile (2)
+  O_FULL = 14,                          // + tile (2)
+  Q_FULL = 16,
+  Q_EMPTY = 17,
+  TAIL = 18,                            // the last value tile of a sequence, before its unused rows are zeroed
+  MMA_DONE = 19,
+  SC_FULL = 20,                         // + scale slot (4)
+  SC_EMPTY = 24,                        // + scale slot (4)
+  NUM_BARS = 28
+};
+
+// Part of a unit that a CTA computes.
+struct Seg {
+  int b, h;
+  int tok;     // first new token of tile A on the packed axis
+  int left;    // new tokens of the sequence from there on
+  int place;   // place of that token
+  int len;
+  int t0, t1;  // key tiles
+  int slot;    // partial sums' slot, or -1: the unit is whole and its rows are final
+};
+
+// Where a CTA's walk along the line stands.
+struct Walk {
+  long long at, x0, x1;  // of the piece [x0, x1)
+  long long start;       // where sequence b begins
+  int b, h, j;
+};
+
+template <int D, bool Q4>
+struct Layout {
+  static constexpr int kQBytes = kT * D * 2;
+  static constexpr int kKVBytes = kT * D * 2;
+  static constexpr int kQ = 0;
+  static constexpr int kKV = 2 * kQBytes;
+  static constexpr int kScale = kKV + slots<Q4>() * kKVBytes;  // per slot {sk, mk'} of the keys, then {sv, mv'}
+  static constexpr int kBars = kScale + (Q4 ? kScaleSlots * kT * 16 : 0);
+  static constexpr int kMisc = kBars + NUM_BARS * 8;
+  static constexpr int kLine = kMisc + 16;  // make_line's and find_seq's sums
+  static constexpr int kWalk = kLine + 18 * 8;
+  static constexpr int kSeg = kWalk + (int)sizeof(Walk);
+  static constexpr int kBytes = kSeg + (int)sizeof(Seg) * (Q4 ? kSegs : 16);
+  static constexpr int kAlloc = kBytes + 1024;
+};
+
+// Sequence b cut into units: pair j holds new tokens [j·d, (j + 1)·d), d = 2·(128 / g).
+// Their weights grow by d, so sums have a closed form.
+struct Units {
+  long long past;  // keys before the new tokens
+  int n, d, pairs;
+  __device__ __forceinline__ Units(const Seq& s, int per_tile) {
+    n = s.n;
+    d = 2 * per_tile;
+    pairs = (n + d - 1) / d;
+    past = max(0, s.len - s.n);
+  }
+  __device__ __forceinline__ long long weight(int j) const { return past + (long long)(j + 1) * d + kUnitKeys; }
+  __device__ __forceinline__ long long before(int j) const {
+    return j * (past + kUnitKeys) + (long long)d * j * (j + 1) / 2;
+  }
+  __device__ __forceinline__ long long head() const { return before(pairs); }
+  // The pair that holds point r of a head's units.
+  __device__ __forceinline__ int find(long long r) const {
+    int lo = 0, hi = pairs - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) / 2;
+      if (before(mid) <= r) lo = mid; else hi = mid - 1;
+    }
+    return lo;
+  }
+};
+
+// Last key tile that `count` tokens from place `place` on see, or -1.
+__device__ __forceinline__ int last_tile(int place, int count) {
+  const int p = place + count - 1;
+  return count > 0 && p >= 0 ? p / kT : -1;
+}
+// Key tiles of pair j of a sequence.
+__device__ __forceinline__ int pair_tiles(const Seq& s, const Units& u, int j) {
+  const int first = j * u.d;
+  return last_tile(s.len - s.n + first, min(u.d, s.n - first)) + 1;
+}
+// Key tiles of a unit that lie before point w of its weight.
+__device__ __forceinline__ int tile_at(int tiles, long long w, long long weight) {
+  return w >= weight ? tiles : (int)(w * tiles / weight);
+}
+
+// The next segments of a CTA's piece (one thread); returns their number.
+__device__ __noinline__ int walk_on(Walk& w, const CacheArgs& c, int per_tile, Seg* segs, int most) {
+  int k = 0;
+  if (w.at >= w.x1) return 0;
+  Seq s = load_seq(c, w.b);
+  while (k < most && w.at < w.x1) {
+    const Units u(s, per_tile);
+    if (w.j >= u.pairs) {
+      w.j = 0;
+      ++w.h;
+    }
+    if (s.n == 0 || w.h >= c.heads) {
+      if (s.n > 0) w.start += u.head() * c.heads;
+      w.h = w.j = 0;
+      s = load_seq(c, ++w.b);
+      continue;
+    }
+    const long long weight = u.weight(w.j);
+    const long long begin = w.start + w.h * u.head() + u.before(w.j), end = begin + weight;
+    const int tiles = pair_tiles(s, u, w.j);
+    const int ta = tile_at(tiles, max(w.at, begin) - begin, weight);
+    const int tb = tile_at(tiles, min(w.x1, end) - begin, weight);
+    if (tiles ? tb > ta : w.at <= begin) {
+      Seg& g = segs[k++];
+      g.b = w.b;
+      g.h = w.h;
+      g.tok = s.first + w.j * u.d;
+      g.left = s.n - w.j * u.d;
+      g.place = s.len - s.n + w.j * u.d;
+      g.len = s.len;
+      g.t0 = ta;
+      g.t1 = tb;
+      g.slot = (ta == 0 && tb == tiles) ? -1 : 2 * (int)blockIdx.x + (begin <= w.x0 ? 0 : 1);
+    }
+    w.at = min(w.x1, end);
+    ++w.j;
+  }
+  return k;
+}
+
+// The clobber keeps these loads where they stand: moved up together they would fill the registers.
+__device__ __forceinline__ float4 ld_shared_f4(uint32_t at) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(at)
+               : "memory");
+  return v;
+}
+
+}  // namespace chunk
+
+template <int D, bool Q4>
+__global__ void __launch_bounds__(chunk::threads<Q4>(), 1)
+    s2_cache_chunk_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                          const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CacheArgs c,
+                          const __grid_constant__ AttnIn in) {
+  using namespace chunk;
+  using L = Layout<D, Q4>;
+  constexpr int kThreads = threads<Q4>();
+  constexpr int kSlots = slots<Q4>();
+  constexpr int kChunks = D / 64;
+  constexpr int kList = Q4 ? kSegs : 16;
+
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sb = smem_u32(smem);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMisc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile int* count = reinterpret_cast<volatile int*>(tmem_slot + 2);
+  long long* line_sh = reinterpret_cast<long long*>(smem + L::kLine);
+  Walk* walk = reinterpret_cast<Walk*>(smem + L::kWalk);
+  Seg* segs = reinterpret_cast<Seg*>(smem + L::kSeg);
+  int* const status = c.status;
+  const uint32_t sbar = sb + L::kBars;
+#define bar(i) (sbar + 8u * (uint32_t)(i))
+#define sQ(x) (sb + L::kQ + (uint32_t)(x) * L::kQBytes)
+#define sKV(slot) (sb + L::kKV + (uint32_t)(slot) * L::kKVBytes)
+
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int per_tile = kT / in.g;  // tokens of a query tile
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kSlots; ++i) {
+      mbar_init(bar(KV_FULL + i), Q4 ? 64 : 1);
+      mbar_init(bar(KV_EMPTY + i), 1);
+    }
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(bar(S_FULL + x), 1);
+      mbar_init(bar(P_FULL + x), 128);
+      mbar_init(bar(O_FULL + x), 1);
+    }
+    mbar_init(bar(Q_FULL), 1);
+    mbar_init(bar(Q_EMPTY), Q4 ? 1 + 256 : 1);
+    mbar_init(bar(TAIL), 1);
+    mbar_init(bar(MMA_DONE), 1);
+    for (int i = 0; i < kScaleSlots; ++i) {
+      mbar_init(bar(SC_FULL + i), 64);
+      mbar_init(bar(SC_EMPTY + i), 256);
+    }
+    *abort_flag = 0;
+    fence_barrier_init();
+    fence_proxy_async_smem();
+  }
+  if (warp == 9) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  // The CTA's piece of the line, and the sequence that it begins in.
+  auto weight_of = [&](int b) -> long long {
+    const Seq s = load_seq(c, b);
+    return s.n > 0 ? Units(s, per_tile).head() * c.heads : 0;
+  };
+  const Line line = make_line<kThreads>(c.B, in.pieces, in.min_piece, line_sh, weight_of);
+  const long long x0 = line.piece * blockIdx.x, x1 = min(x0 + line.piece, line.total);
+  int b_first = -1;
+  long long b_start = 0;
+  if (x0 < x1) find_seq<kThreads>(c.B, x0, line_sh, weight_of, b_first, b_start);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  // Thread 0's walk along the line; its state is in shared memory, the registers are the softmax's.
+  if (threadIdx.x == 0) {
+    walk->b = walk->h = walk->j = 0;
+    walk->at = x0;
+    walk->x0 = x0;
+    walk->x1 = max(x0, x1);
+    walk->start = b_start;
+    if (x0 < x1) {
+      const Units u(load_seq(c, b_first), per_tile);
+      walk->b = b_first;
+      walk->h = (int)((x0 - b_start) / u.head());
+      walk->j = u.find((x0 - b_start) % u.head());
+    }
+  }
+
+  // Counters that run on from segment to segment (each role keeps those it uses).
+  int e = 0;                  // key and value tiles so far: e-th goes to slot e % kSlots
+  int n_seg = 0;              // segments with keys
+  int nA = 0, nB = 0;         // key tiles of each query tile
+  int oA = 0, oB = 0;         // segments in which each query tile had keys
+  int n_sc = 0;               // key tiles (scale slots)
+  int n_tail = 0;
+  bool ok = true;
+
+  while (true) {
+    // ------------------------------------------------------------ the next segments
+    if (threadIdx.x == 0) *count = *abort_flag ? 0 : walk_on(*walk, c, per_tile, segs, kList);
+    __syncthreads();
+    const int k_segs = *count;
+    if (k_segs == 0) break;
+
+    for (int si = 0; si < k_segs && ok; ++si) {
+      const Seg g = segs[si];
+      const int cntA = min(g.left, per_tile), cntB = min(g.left - per_tile, per_tile);
+      const int lastA = min(last_tile(g.place, cntA), g.t1 - 1);
+      const int lastB = min(last_tile(g.place + per_tile, cntB), g.t1 - 1);
+      const bool hasA = lastA >= g.t0, hasB = lastB >= g.t0;
+      const bool keys = g.t1 > g.t0;
+
+      if (warp == 8) {
+        // -------------------------------------------------------- TMA
+        if (!keys) continue;
+        if (lane == 0) {
+          if (n_seg > 0) ok = s2_wait(bar(Q_EMPTY), (n_seg - 1) & 1, abort_flag, status, 1);
+          if (ok) {
+            const uint32_t bytes = (uint32_t)(per_tile * in.g) * 128 * kChunks;
+            mbar_arrive_expect_tx(bar(Q_FULL), (hasA ? bytes : 0) + (hasB ? bytes : 0));
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+              if (x ? hasB : hasA)
+                for (int ch = 0; ch < kChunks; ++ch)
+                  tma_load_3d(sQ(x) + ch * kChunkBytes, &tmQ, ch * 64, g.h * in.g, g.tok + x * per_tile, bar(Q_FULL));
+          }
+        }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        ++n_seg;
+        if constexpr (!Q4) {
+          const int pages = kT >> c.log2s;  // of a tile
+          for (int t = g.t0; t < g.t1 && ok; ++t) {
+            const int live = min(pages, ((g.len - t * kT - 1) >> c.log2s) + 1);
+            int page = 0;
+            if (lane < live) page = page_of(c, g.b, t * kT + (lane << c.log2s));
+            const bool tail = g.len - t * kT < kT;
+#pragma unroll
+            for (int v = 0; v < 2; ++v) {
+              const int slot = e % kSlots;
+              if (e >= kSlots) ok = s2_wait(bar(KV_EMPTY + slot), ((e / kSlots) - 1) & 1, abort_flag, status, 1);
+              ok = __all_sync(0xffffffffu, ok);
+              if (!ok) break;
+              const uint32_t full = v && tail ? bar(TAIL) : bar(KV_FULL + slot);
+              if (lane == 0) mbar_arrive_expect_tx(full, (uint32_t)(live << c.log2s) * 128 * kChunks);
+              __syncwarp();
+              if (lane < live) {
+                for (int ch = 0; ch < kChunks; ++ch)
+                  tma_load_3d(sKV(slot) + ch * kChunkBytes + ((lane << c.log2s) * 128), v ? &tmV : &tmK, ch * 64, 0,
+                              page * c.heads + g.h, full);
+              }
+              if (v && tail) {
+                // rows behind the sequence may hold anything, and 0 times a NaN is a NaN
+                if (!s2_wait_drain(bar(TAIL), n_tail & 1, status, 1)) *abort_flag = 1;
+                ++n_tail;
+                const int used = g.len - t * kT;
+                for (int i = used * 8 * kChunks + lane; i < kT * 8 * kChunks; i += 32) {
+                  const int row = i / (8 * kChunks), piece = i % (8 * kChunks);
+                  st_shared_v4(sKV(slot) + (piece / 8) * kChunkBytes + row * 128 + (piece % 8) * 16, 0u, 0u, 0u, 0u);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(KV_FULL + slot));
+              }
+              ++e;
+            }
+          }
+        }
+      } else if (warp == 9) {
+        // -------------------------------------------------------- MMA
+        if (lane == 0 && keys) {
+          constexpr uint32_t idesc_qk = umma_idesc_bf16(128, 128, 0, 0);
+          constexpr uint32_t idesc_pv = umma_idesc_bf16(128, D, 0, 1);
+#define ISSUE_QK(x, slot)                                                                              \
+  do {                                                                                                 \
+    const uint64_t a0_ = umma_desc_sw128(sQ(x), 16, 1024), b0_ = umma_desc_sw128(sKV(slot), 16, 1024); \
+    _Pragma("unroll") for (int kk = 0; kk < D / 16; ++kk) {                                            \
+      const uint64_t off_ = ((kk / 4) * kChunkBytes + (kk % 4) * 32) >> 4;                             \
+      umma_ss(tmem + (x) * 128, a0_ + off_, b0_ + off_, idesc_qk, kk > 0);                             \
+    }                                                                                                  \
+  } while (0)
+#define ISSUE_PV(x, slot, acc)                                                                  \
+  do {                                                                                          \
+    const uint64_t b0_ = umma_desc_sw128(sKV(slot), kChunkBytes, 1024);                         \
+    _Pragma("unroll") for (int kk = 0; kk < kT / 16; ++kk) {                                    \
+      umma_ts(tmem + 256 + (x) * D, tmem + (x) * 128 + 8 * kk, b0_ + (uint64_t)(kk * 2048 >> 4), \
+              idesc_pv, ((acc) || kk > 0) ? 1u : 0u);                                           \
+    }                                                                                           \
+  } while (0)
+#define WAIT_KV(i) s2_wait(bar(KV_FULL + (i) % kSlots), ((i) / kSlots) & 1, abort_flag, status, 2)
+          ok = s2_wait(bar(Q_FULL), n_seg & 1, abort_flag, status, 2);
+          ++n_seg;
+          int eK = e++;
+          if (ok) ok = WAIT_KV(eK);
+          if (ok) {
+            if (hasA) {
+              ISSUE_QK(0, eK % kSlots);
+              umma_commit(bar(S_FULL + 0));
+            }
+            if (hasB) {
+              ISSUE_QK(1, eK % kSlots);
+              umma_commit(bar(S_FULL + 1));
+            }
+            umma_commit(bar(KV_EMPTY + eK % kSlots));
+            if (g.t1 - g.t0 == 1) umma_commit(bar(Q_EMPTY));
+          }
+          for (int t = g.t0; t < g.t1 && ok; ++t) {
+            const bool more = t + 1 < g.t1;
+            const int eV = e++;
+            eK = more ? e++ : 0;
+            ok = WAIT_KV(eV);
+            if (ok && more) ok = WAIT_KV(eK);
+            if (!ok) break;
+            const int sV = eV % kSlots, sK = eK % kSlots;
+            if (t <= lastA) {
+              ok = s2_wait(bar(P_FULL + 0), nA & 1, abort_flag, status, 2);
+              if (!ok) break;
+              tc_fence_after();
+              ISSUE_PV(0, sV, t > g.t0);
+              ++nA;
+            }
+            if (more && t + 1 <= lastA) {
+              ISSUE_QK(0, sK);
+              umma_commit(bar(S_FULL + 0));
+            }
+            if (t <= lastB) {
+              ok = s2_wait(bar(P_FULL + 1), nB & 1, abort_flag, status, 2);
+              if (!ok) break;
+              tc_fence_after();
+              ISSUE_PV(1, sV, t > g.t0);
+              ++nB;
+            }
+            if (more && t + 1 <= lastB) {
+              ISSUE_QK(1, sK);
+              umma_commit(bar(S_FULL + 1));
+            }
+            umma_commit(bar(KV_EMPTY + sV));
+            if (more) {
+              umma_commit(bar(KV_EMPTY + sK));
+              if (t + 2 == g.t1) umma_commit(bar(Q_EMPTY));
+            }
+          }
+          if (ok && hasA) umma_commit(bar(O_FULL + 0));
+          if (ok && hasB) umma_commit(bar(O_FULL + 1));
+        }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+      } else if (Q4 && warp >= 10) {
+        // -------------------------------------------------------- unpacking of 4-bit pages
+        // A thread takes rows `row` and `row + 64` of each tile; the next tile's codes are on
+        // their way while this one's are unpacked.
+        if (!keys) continue;
+        const int row = threadIdx.x - 320;
+        constexpr int kWords = D / 8;  // of a row's codes
+        uint32_t wa[kWords], wb[kWords];  // rows `row`, `row + 64`: one is unpacked, one is on its way
+        size_t at[2];
+        bool use[2];
+        auto place = [&](int t) {
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const int p = t * kT + row + 64 * y;
+            use[y] = p < g.len;
+            at[y] = use[y] ? row_of(c, page_of(c, g.b, p), g.h, p) : 0;
+          }
+        };
+        auto fetch = [&](const void* codes, int y, uint32_t (&w)[kWords]) {
+          const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(codes) + at[y] * (D / 2));
+#pragma unroll
+          for (int i = 0; i < kWords / 4; ++i) {
+            uint4 x = make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);  // codes 8: zeros
+            if (use[y]) x = __ldg(src + i);
+            w[4 * i] = x.x, w[4 * i + 1] = x.y, w[4 * i + 2] = x.z, w[4 * i + 3] = x.w;
+          }
+        };
+        auto store = [&](const uint32_t (&w)[kWords], int y, int slot) {
+          // a word's 4 bytes are channels 4i .. 4i + 3 (low halves) and D/2 + 4i .. (high halves)
+#pragma unroll
+          for (int i = 0; i < kWords; i += 2)
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              uint32_t o[4];
+#pragma unroll
+              for (int z = 0; z < 2; ++z) {
+                const uint32_t x = (w[i + z] >> (4 * half)) & 0x0f0f0f0fu;
+                o[2 * z] = less_136(__byte_perm(x, 0x43u, 0x4140));
+                o[2 * z + 1] = less_136(__byte_perm(x, 0x43u, 0x4342));
+              }
+              const int ch = half * (D / 2) + 4 * i, piece = (ch % 64) / 8;
+              st_shared_v4(sKV(slot) + (ch / 64) * kChunkBytes + (row + 64 * y) * 128 + ((piece ^ (row & 7)) << 4),
+                           o[0], o[1], o[2], o[3]);
+            }
+        };
+        auto claim = [&]() -> int {  // the next tile's slot, once its products are done
+          const int slot = e % kSlots;
+          if (e >= kSlots) ok = s2_wait(bar(KV_EMPTY + slot), ((e / kSlots) - 1) & 1, abort_flag, status, 8);
+          ++e;
+          return slot;
+        };
+        place(g.t0);
+        fetch(c.k, 0, wa);
+        for (int t = g.t0; t < g.t1; ++t) {
+          fetch(c.k, 1, wb);
+          const int sK = claim();
+          if (!ok) break;
+          store(wa, 0, sK);
+          fetch(c.v, 0, wa);
+          store(wb, 1, sK);
+          fence_proxy_async_smem();
+          mbar_arrive(bar(KV_FULL + sK));
+          fetch(c.v, 1, wb);
+          const int sc = n_sc % kScaleSlots;
+          if (n_sc >= kScaleSlots)
+            ok = s2_wait(bar(SC_EMPTY + sc), ((n_sc / kScaleSlots) - 1) & 1, abort_flag, status, 8);
+          if (!ok) break;
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const float2 k2 = q4_pair(use[y] ? __ldg(static_cast<const uint32_t*>(c.k_scale) + at[y]) : 0u);
+            const float2 v2 = q4_pair(use[y] ? __ldg(static_cast<const uint32_t*>(c.v_scale) + at[y]) : 0u);
+            float2* to = reinterpret_cast<float2*>(smem + L::kScale) + sc * 2 * kT + row + 64 * y;
+            to[0] = make_float2(k2.x, fmaf(8.f, k2.x, k2.y));
+            to[kT] = make_float2(v2.x, fmaf(8.f, v2.x, v2.y));
+          }
+          mbar_arrive(bar(SC_FULL + sc));
+          ++n_sc;
+          const int sV = claim();
+          if (!ok) break;
+          store(wa, 0, sV);
+          if (t + 1 < g.t1) {
+            place(t + 1);
+            fetch(c.k, 0, wa);
+          }
+          store(wb, 1, sV);
+          fence_proxy_async_smem();
+          mbar_arrive(bar(KV_FULL + sV));
+        }
+      } else if (warp < 8) {
+        // -------------------------------------------------------- softmax
+        const int x = warp / 4, wq = warp % 4;
+        const int r = wq * 32 + lane;  // row of the tile == TMEM lane
+        const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
+        const uint32_t tS = tmem + lane_off + x * 128;
+        const uint32_t tO = tmem + lane_off + 256 + x * D;
+        const bool has = x ? hasB : hasA;
+        const int last = x ? lastB : lastA, cnt = x ? cntB : cntA;
+        int& nS = x ? nB : nA;
+        int& nO = x ? oB : oA;
+        const int tok = r / in.g;  // of the tile
+        const bool live = tok < cnt;
+        // rows of no token see all of their tile; they are not stored
+        const int place = g.place + x * per_tile + (live ? tok : max(cnt, 1) - 1);
+        float m_used = -INFINITY, l = 0.f;
+        float vsum = 0.f, qsum = 0.f;
+        if (Q4 && keys) {
+          ok = s2_wait(bar(Q_FULL), n_seg & 1, abort_flag, status, 4);
+          ++n_seg;
+          if (ok && has && live) {
+            for (int i = 0; i < 8 * kChunks; ++i) {
+              const uint32_t at = sQ(x) + (i / 8) * kChunkBytes + r * 128 + (((i % 8) ^ (r & 7)) << 4);
+              uint32_t w[4];
+              asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                           : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                           : "r"(at));
+#pragma unroll
+              for (int z = 0; z < 4; ++z)
+                qsum += __uint_as_float(w[z] << 16) + __uint_as_float(w[z] & 0xffff0000u);
+            }
+          }
+          mbar_arrive(bar(Q_EMPTY));
+        }
+        for (int t = g.t0; t < g.t1 && ok; ++t) {
+          const int sc = n_sc % kScaleSlots;
+          if (t > last) {
+            if constexpr (Q4) {
+              // the other tile's keys: only counted
+              ok = s2_wait(bar(SC_FULL + sc), (n_sc / kScaleSlots) & 1, abort_flag, status, 4);
+              if (ok) mbar_arrive(bar(SC_EMPTY + sc));
+              ++n_sc;
+              continue;
+            } else {
+              break;
+            }
+          }
+          ok = s2_wait(bar(S_FULL + x), nS & 1, abort_flag, status, 4);
+          if constexpr (Q4) {
+            if (ok) ok = s2_wait(bar(SC_FULL + sc), (n_sc / kScaleSlots) & 1, abort_flag, status, 4);
+          }
+          if (!ok) break;
+          tc_fence_after();
+          ++nS;
+          uint32_t s[kT];
+          if constexpr (Q4) {
+            tmem_ld64(tS, *reinterpret_cast<uint32_t(*)[64]>(&s[0]));
+            tmem_ld64(tS + 64, *reinterpret_cast<uint32_t(*)[64]>(&s[64]));
+          } else {
+            tmem_ld128(tS, s);
+          }
+          tmem_wait_ld();
+          const uint32_t scales = sb + L::kScale + sc * 2 * kT * 8;  // {scale, min + 8 scale} of the keys, the values
+          if constexpr (Q4) {
+            const float2 q2 = make_float2(qsum, qsum);
+#pragma unroll
+            for (int col = 0; col < kT; col += 2) {
+              const float4 a = ld_shared_f4(scales + col * 8);
+              const float2 v = __ffma2_rn(make_float2(__uint_as_float(s[col]), __uint_as_float(s[col + 1])),
+                                          make_float2(a.x, a.z), __fmul2_rn(make_float2(a.y, a.w), q2));
+              s[col] = __float_as_uint(v.x);
+              s[col + 1] = __float_as_uint(v.y);
+            }
+          }
+          const int cmax = min(kT, max(0, place + 1 - t * kT));
+          if (!__all_sync(0xffffffffu, cmax == kT)) {
+#pragma unroll
+            for (int col = 0; col < kT; ++col)
+              if (col >= cmax) s[col] = 0xff800000u;  // -inf
+          }
+          float mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int col = 0; col < kT; col += 8) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              mq[q] = fmax3(mq[q], __uint_as_float(s[col + 2 * q]), __uint_as_float(s[col + 2 * q + 1]));
+          }
+          const float mx = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3])) * in.scale_log2;
+          const float m_new = fmaxf(m_used, mx);
+          const bool need = m_new > m_used + 8.0f;
+          float factor = 1.f;
+          if (need) {
+            factor = ex2(m_used - m_new);
+            l *= factor;
+            vsum *= factor;
+            m_used = m_new;
+          }
+          const float m_exp = (m_used == -INFINITY) ? 0.f : m_used;
+          const float2 c2 = make_float2(in.scale_log2, in.scale_log2);
+          const float2 nm2 = make_float2(-m_exp, -m_exp);
+          float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+          float2 vacc = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int col = 0; col < kT; col += 2) {
+            const float2 a =
+                __ffma2_rn(make_float2(__uint_as_float(s[col]), __uint_as_float(s[col + 1])), c2, nm2);
+            float2 p = make_float2(ex2(a.x), ex2(a.y));
+            acc[(col / 2) & 3] = __fadd2_rn(acc[(col / 2) & 3], p);
+            if constexpr (Q4) {
+              const float4 u = ld_shared_f4(scales + (kT + col) * 8);
+              vacc = __ffma2_rn(p, make_float2(u.y, u.w), vacc);
+              p = __fmul2_rn(p, make_float2(u.x, u.z));
+            }
+            s[col / 2] = pack_bf16(p.x, p.y);
+          }
+          const float2 sum = __fadd2_rn(__fadd2_rn(acc[0], acc[1]), __fadd2_rn(acc[2], acc[3]));
+          l += sum.x + sum.y;
+          vsum += vacc.x + vacc.y;
+          if constexpr (Q4) {
+            mbar_arrive(bar(SC_EMPTY + sc));
+            ++n_sc;
+          }
+          // S(t) was issued behind O += P V of tile t - 1, so O is complete here
+          if (t > g.t0 && __any_sync(0xffffffffu, need)) {
+            const float f = need ? factor : 1.f;
+#pragma unroll
+            for (int j = 0; j < D / 32; ++j) {
+              uint32_t o[32];
+              tmem_ld32(tO + j * 32, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+              tmem_st32(tO + j * 32, o);
+            }
+            tmem_wait_st();
+          }
+          tmem_st64(tS, *reinterpret_cast<const uint32_t(*)[64]>(&s[0]));
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(bar(P_FULL + x));
+        }
+        if (ok && has) {
+          ok = s2_wait(bar(O_FULL + x), nO & 1, abort_flag, status, 4);
+          ++nO;
+          tc_fence_after();
+        }
+        // ------------------------------------------------------ rows out
+        if (ok) {
+          const size_t out = (size_t)(g.tok + x * per_tile + tok) * in.heads + g.h * in.g + r % in.g;
+          const float inv = l > 0.f ? 1.f / l : 0.f;
+          float* part = in.partial + ((size_t)g.slot * 2 * kT + x * kT + r) * (D + 4);
+#pragma unroll
+          for (int j = 0; j < D / 32; ++j) {
+            uint32_t o[32];
+            if (has) {
+              tmem_ld32(tO + j * 32, o);
+              tmem_wait_ld();
+            } else {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = 0u;
+            }
+            if (live) {
+              if (g.slot < 0) {
+                uint4* dst = reinterpret_cast<uint4*>(in.o + out * D + j * 32);
+#pragma unroll
+                for (int i = 0; i < 32; i += 8) {
+                  uint32_t w[4];
+#pragma unroll
+                  for (int z = 0; z < 4; ++z)
+                    w[z] = pack_bf16((__uint_as_float(o[i + 2 * z]) + vsum) * inv,
+                                     (__uint_as_float(o[i + 2 * z + 1]) + vsum) * inv);
+                  dst[i / 8] = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+              } else {
+                float4* dst = reinterpret_cast<float4*>(part + j * 32);
+#pragma unroll
+                for (int i = 0; i < 32; i += 4)
+                  dst[i / 4] = make_float4(__uint_as_float(o[i]) + vsum, __uint_as_float(o[i + 1]) + vsum,
+                                           __uint_as_float(o[i + 2]) + vsum, __uint_as_float(o[i + 3]) + vsum);
+              }
+            }
+          }
+          if (live) {
+            if (g.slot < 0) {
+              if (in.lse) in.lse[out] = l > 0.f ? (m_used + log2f(l)) * 0.69314718055994531f : -INFINITY;
+            } else {
+              *reinterpret_cast<float4*>(part + D) = make_float4(m_used, l, 0.f, 0.f);
+            }
+          }
+          tc_fence_before();  // O has been read: ordered before the next unit's first P_FULL arrival
+        }
+      }
+    }
+    __syncthreads();
+  }
+
+  // Copies and products in flight land before shared and tensor memory are released (also after an abort).
+  if (warp == 8 && lane == 0) {
+    if constexpr (!Q4) {
+      for (int d = (e > kSlots ? e - kSlots : 0); d < e; ++d)
+        s2_wait_drain(bar(KV_FULL + d % kSlots), (d / kSlots) & 1, status, 1);
+    }
+    if (n_seg > 0) s2_wait_drain(bar(Q_FULL), (n_seg - 1) & 1, status, 1);
+  }
+  if (warp == 9 && lane == 0) {
+    umma_commit(bar(MMA_DONE));
+    s2_wait_drain(bar(MMA_DONE), 0, status, 2);
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+#undef ISSUE_QK
+#undef ISSUE_PV
+#undef WAIT_KV
+#undef bar
+#undef sQ
+#undef sKV
+
+// Joins the partial sums of units that the line's cuts run through: blocks
+// (i, y) stand for cut i + 1, and share the unit's rows with the blocks of its
+// other cuts.  A warp takes a row; the order of the sum is the pieces'.
+template <int D>
+__global__ void __launch_bounds__(256) s2_cache_chunk_join_kernel(const __grid_constant__ CacheArgs c,
+                                                                  const __grid_constant__ AttnIn in) {
+  using namespace chunk;
+  constexpr int kThreads = 256;
+  __shared__ long long sh[kThreads / 32 + 2];
+  const int per_tile = kT / in.g;
+  auto weight_of = [&](int b) -> long long {
+    const Seq s = load_seq(c, b);
+    return s.n > 0 ? Units(s, per_tile).head() * c.heads : 0;
+  };
+  const Line line = make_line<kThreads>(c.B, in.pieces, in.min_piece, sh, weight_of);
+  const long long cut = line.piece * (blockIdx.x + 1);
+  if (cut >= line.total) return;
+  int b;
+  long long start;
+  find_seq<kThreads>(c.B, cut, sh, weight_of, b, start);
+  const Seq s = load_seq(c, b);
+  const Units u(s, per_tile);
+  const int h = (int)((cut - start) / u.head());
+  const int j = u.find((cut - start) % u.head());
+  const long long begin = start + h * u.head() + u.before(j), w = u.weight(j);
+  if (begin == cut) return;
+  const int tiles = pair_tiles(s, u, j);
+  if (tiles == 0) return;
+  const int p0 = (int)(begin / line.piece), p1 = (int)((begin + w - 1) / line.piece);
+  auto first_tile = [&](int p) { return tile_at(tiles, max(line.piece * p, begin) - begin, w); };
+  auto end_tile = [&](int p) { return tile_at(tiles, min(line.piece * (p + 1), begin + w) - begin, w); };
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int left = s.n - j * u.d;
+  const int workers = (p1 - p0) * gridDim.y * (kThreads / 32);
+  const int me = (((int)blockIdx.x - p0) * gridDim.y + blockIdx.y) * (kThreads / 32) + warp;
+  constexpr int kV = D / 32;  // channels of a lane
+  for (int i = me; i < min(left, u.d) * in.g; i += workers) {
+    const int tok = i / in.g, head = i % in.g;
+    const int row = (tok / per_tile) * kT + (tok % per_tile) * in.g + head;
+    float mm = -INFINITY, ll = 0.f, o[kV] = {};
+    for (int p = p0; p <= p1; ++p) {
+      const int ta = first_tile(p), tb = end_tile(p);
+      if (ta == tb) continue;
+      if (ta == 0 && tb == tiles) return;  // one piece had all of the unit's tiles and wrote its rows
+      const float* part =
+          in.partial + ((size_t)(2 * p + (begin <= line.piece * p ? 0 : 1)) * 2 * kT + row) * (D + 4);
+      const float2 ml = *reinterpret_cast<const float2*>(part + D);
+      float v[kV];
+      if constexpr (kV == 4) {
+        const float4 t = *reinterpret_cast<const float4*>(part + 4 * lane);
+        v[0] = t.x, v[1] = t.y, v[2] = t.z, v[3] = t.w;
+      } else {
+        const float2 t = *reinterpret_cast<const float2*>(part + 2 * lane);
+        v[0] = t.x, v[1] = t.y;
+      }
+      if (ml.x == -INFINITY) continue;
+      const float m = fmaxf(mm, ml.x);
+      const float f0 = ex2(mm - m), f1 = ex2(ml.x - m);
+      ll = ll * f0 + ml.y * f1;
+#pragma unroll
+      for (int z = 0; z < kV; ++z) o[z] = o[z] * f0 + v[z] * f1;
+      mm = m;
+    }
+    const float inv = ll > 0.f ? 1.f / ll : 0.f;
+    const size_t out = (size_t)(s.first + j * u.d + tok) * in.heads + h * in.g + head;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(in.o + out * D) + lane * (kV / 2);
+    if constexpr (kV == 4)
+      *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv));
+    else
+      *dst = pack_bf16(o[0] * inv, o[1] * inv);
+    if (in.lse && lane == 0) in.lse[out] = ll > 0.f ? (mm + log2f(ll)) * 0.69314718055994531f : -INFINITY;
+  }
+}
+
+template <int D, bool Q4>
+static int chunk_impl(const CUtensorMap* tq, const CUtensorMap* tk, const CUtensorMap* tv, const CacheArgs& c,
+                      const AttnIn& in, cudaStream_t stream) {
+  using L = chunk::Layout<D, Q4>;
+  static_assert(L::kAlloc <= 232448, "shared memory budget");
+  cudaError_t e =
+      cudaFuncSetAttribute(s2_cache_chunk_kernel<D, Q4>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
+  if (e != cudaSuccess) return (int)e;
+  s2_cache_chunk_kernel<D, Q4><<<in.pieces, chunk::threads<Q4>(), L::kAlloc, stream>>>(*tq, *tk, *tv, c, in);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return (int)e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(in.pieces - 1, 4);
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return (int)cudaLaunchKernelEx(&cfg, s2_cache_chunk_join_kernel<D>, c, in);
+}
+
+int launch_cache_chunk(const CUtensorMap* tq, const CUtensorMap* tk, const CUtensorMap* tv, const CacheArgs& c,
+                       const AttnIn& in, int D, bool q4, cudaStream_t stream) {
+  if (D == 64)
+    return q4 ? chunk_impl<64, true>(tq, tk, tv, c, in, stream) : chunk_impl<64, false>(tq, tk, tv, c, in, stream);
+  return q4 ? chunk_impl<128, true>(tq, tk, tv, c, in, stream) : chunk_impl<128, false>(tq, tk, tv, c, in, stream);
+}
+
+size_t cache_chunk_partial_bytes(int D) {
+  return (size_t)2 * kChunkPieces * 2 * chunk::kT * (D + 4) * sizeof(float);
+}
+
+}  // namespace s2

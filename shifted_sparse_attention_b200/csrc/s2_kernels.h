@@ -78,6 +78,10 @@ int launch_doc_bounds(const int32_t* ids, int32_t* bounds, int B, int N, cudaStr
 
 // Per-device set-up on first use (capability check): the status word's address, or an error code.
 int device_status(int** status);
+// Tensor map of a contiguous-rows bf16 tensor of 3 dimensions, innermost first (strides in bytes of dimensions 1, 2),
+// with 128-byte swizzled boxes of 64 x box1 x box2.
+int encode_map(CUtensorMap* m, const void* base, const uint64_t (&dims)[3], const uint64_t (&strides)[2],
+               uint32_t box1, uint32_t box2);
 
 // Paged cache (s2_cache.cuh): new rows in, rows back out, attention over it.
 struct AppendIn {
@@ -109,5 +113,10 @@ int launch_cache_read(const CacheArgs& c, int D, bool q4, void* k_out, void* v_o
 // rows: query rows of a unit at most, as far as the caller knows (a choice of tile only)
 int launch_cache_decode(const CacheArgs& c, const AttnIn& in, int D, bool q4, int rows, cudaStream_t stream);
 size_t cache_decode_partial_bytes(int D);
+
+constexpr int kChunkPieces = 148;  // CTAs of the chunk kernel: one on each SM
+int launch_cache_chunk(const CUtensorMap* tq, const CUtensorMap* tk, const CUtensorMap* tv, const CacheArgs& c,
+                       const AttnIn& in, int D, bool q4, cudaStream_t stream);
+size_t cache_chunk_partial_bytes(int D);
 
 }  // namespace s2

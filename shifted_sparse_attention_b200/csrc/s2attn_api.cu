@@ -180,6 +180,20 @@ int device_status(int** status) {
   return rc;
 }
 
+int encode_map(CUtensorMap* m, const void* base, const uint64_t (&dims)[3], const uint64_t (&strides)[2],
+               uint32_t box1, uint32_t box2) {
+  DeviceState* st = nullptr;
+  const int rc = device_state(&st);
+  if (rc) return rc;
+  const cuuint64_t d[3] = {dims[0], dims[1], dims[2]}, str[2] = {strides[0], strides[1]};
+  const cuuint32_t box[3] = {64, box1, box2}, elem[3] = {1, 1, 1};
+  const CUresult r = st->encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), d, str, box, elem,
+                                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(S2_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+  return S2_OK;
+}
+
 // Records a message for s2attn_last_error() from other translation units.
 int report_error(int code, const char* fmt, ...) {
   char buf[512];

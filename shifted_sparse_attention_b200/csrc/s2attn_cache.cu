@@ -89,6 +89,15 @@ int check_heads(const s2_cache* cache, int64_t heads) {
   return S2_OK;
 }
 
+// Query rows that share a key/value head in one sequence, as far as the host knows.
+int64_t shared_rows(const s2_cache* cache, const s2_cache_batch* batch, int64_t heads) {
+  const int64_t n = batch->max_new ? batch->max_new : (batch->tokens + batch->seqs - 1) / batch->seqs;
+  return n * (heads / cache->heads);
+}
+
+// Up to this many, the cache's bytes bound the call (s2_cache_attn.cu); beyond, the products (s2_cache_chunk.cu).
+constexpr int64_t kFewRows = 32;
+
 int launched(int rc, const char* what) {
   if (rc == 0) return S2_OK;
   return report_error(S2_ERR_CUDA, "%s launch failed: %s", what, cudaGetErrorString((cudaError_t)rc));
@@ -150,7 +159,8 @@ int s2attn_cache_read(const s2_cache* cache, const s2_cache_batch* batch, void* 
 size_t s2attn_cache_attn_workspace_size(const s2_cache* cache, const s2_cache_batch* batch, int64_t heads) {
   s2::CacheArgs a;
   if (take(cache, batch, &a) != S2_OK || check_heads(cache, heads) != S2_OK) return 0;
-  return s2::cache_decode_partial_bytes((int)cache->D);
+  return shared_rows(cache, batch, heads) <= kFewRows ? s2::cache_decode_partial_bytes((int)cache->D)
+                                                      : s2::cache_chunk_partial_bytes((int)cache->D);
 }
 
 int s2attn_cache_attn(const s2_cache* cache, const s2_cache_batch* batch, const void* q, int64_t ldq, void* o,
@@ -180,11 +190,29 @@ int s2attn_cache_attn(const s2_cache* cache, const s2_cache_batch* batch, const 
   in.heads = (int)heads;
   in.g = (int)(heads / cache->heads);
   in.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)D));
-  in.pieces = s2::kDecodePieces;
-  in.min_piece = 16;
-  const int64_t rows = (batch->max_new ? batch->max_new : batch->tokens) * in.g;
-  return launched(s2::launch_cache_decode(a, in, (int)D, cache->format == S2_CACHE_Q4, rows > 16 ? 16 : (int)rows,
-                                          static_cast<cudaStream_t>(stream)),
+  const bool q4 = cache->format == S2_CACHE_Q4;
+  const int64_t rows = shared_rows(cache, batch, heads);
+  if (rows <= kFewRows) {
+    in.pieces = s2::kDecodePieces;
+    in.min_piece = 16;
+    return launched(s2::launch_cache_decode(a, in, (int)D, q4, rows > 16 ? 16 : (int)rows,
+                                            static_cast<cudaStream_t>(stream)),
+                    "cache attention");
+  }
+  in.pieces = s2::kChunkPieces;
+  in.min_piece = 512;
+  const uint64_t S = (uint64_t)cache->page_size, d = (uint64_t)D, blocks = (uint64_t)(cache->pages * cache->heads);
+  CUtensorMap tq, tk, tv;
+  if ((rc = s2::encode_map(&tq, q, {d, (uint64_t)heads, (uint64_t)batch->tokens}, {d * 2, (uint64_t)ldq * 2},
+                           (uint32_t)in.g, (uint32_t)(128 / in.g))))
+    return rc;
+  if (q4) {
+    tk = tv = tq;  // 4-bit pages are not read through tensor maps
+  } else if ((rc = s2::encode_map(&tk, cache->k, {d, S, blocks}, {d * 2, S * d * 2}, (uint32_t)S, 1)) ||
+             (rc = s2::encode_map(&tv, cache->v, {d, S, blocks}, {d * 2, S * d * 2}, (uint32_t)S, 1))) {
+    return rc;
+  }
+  return launched(s2::launch_cache_chunk(&tq, &tk, &tv, a, in, (int)D, q4, static_cast<cudaStream_t>(stream)),
                   "cache attention");
 }
 
