@@ -150,6 +150,50 @@ __device__ __forceinline__ void find_seq(int B, long long x, long long* sh, Weig
   first_out = 0;
 }
 
+// Both at once for piece `index`: the line, and the sequence that holds the piece's first point (or -1).
+template <int kThreads, typename Weight>
+__device__ __forceinline__ Line find_piece(int B, int pieces, long long min_piece, int index, long long* sh,
+                                           Weight weight, int& b_out, long long& first_out) {
+  constexpr int kW = kThreads / 32;
+  b_out = -1;
+  first_out = 0;
+  if (B > kThreads) {
+    const Line l = make_line<kThreads>(B, pieces, min_piece, sh, weight);
+    if (l.piece * index < l.total) find_seq<kThreads>(B, l.piece * index, sh, weight, b_out, first_out);
+    return l;
+  }
+  // one look at the lengths: a thread per sequence
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const long long mine = (int)threadIdx.x < B ? weight((int)threadIdx.x) : 0;
+  long long end = mine;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, end, off);
+    if (lane >= off) end += y;
+  }
+  if (lane == 31) sh[warp] = end;
+  if (threadIdx.x == 0) sh[kW] = -1;
+  __syncthreads();
+  Line l;
+  l.total = 0;
+#pragma unroll
+  for (int w = 0; w < kW; ++w) {
+    if (w < warp) end += sh[w];
+    l.total += sh[w];
+  }
+  l.piece = (l.total + pieces - 1) / pieces;
+  if (l.piece < min_piece) l.piece = min_piece;
+  const long long x = l.piece * index;
+  if (x < end && x >= end - mine) {
+    sh[kW] = (int)threadIdx.x;
+    sh[kW + 1] = end - mine;
+  }
+  __syncthreads();
+  b_out = (int)sh[kW];
+  first_out = sh[kW + 1];
+  return l;
+}
+
 // ---------------------------------------------------------------- 4-bit codes as bf16
 // Two codes (bits [0,4) and [16,20) of x) as bf16 code - 8: 0x4300 | c is 128 + c.
 __device__ __forceinline__ uint32_t less_136(uint32_t y) {
@@ -157,6 +201,7 @@ __device__ __forceinline__ uint32_t less_136(uint32_t y) {
   const __nv_bfloat162 z = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&y), off);
   return *reinterpret_cast<const uint32_t*>(&z);
 }
-__device__ __forceinline__ uint32_t codes_bf16(uint32_t x) { return less_136((x & 0x000f000fu) | 0x43004300u); }
+__device__ __forceinline__ uint32_t codes_128(uint32_t x) { return (x & 0x000f000fu) | 0x43004300u; }  // 128 + code
+__device__ __forceinline__ uint32_t codes_bf16(uint32_t x) { return less_136(codes_128(x)); }
 
 }  // namespace s2

@@ -41,9 +41,6 @@ namespace s2 {
 
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kThreads = kWarps * 32;
-
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -101,13 +98,14 @@ struct ValueRegs<D, true> {
   uint32_t pair[2];       // of keys r, r + 8
 };
 
+// A lane's place in a block of rows: bytes from the block's first row, for keys and for values.
 template <int D, bool Q4>
-__device__ __forceinline__ void load_keys(KeyRegs<D, Q4>& x, const CacheArgs& c, size_t row, int r, int cc) {
+__device__ __forceinline__ void load_keys(KeyRegs<D, Q4>& x, const uint8_t* rows, const uint8_t* pairs) {
+  constexpr int kRow = Q4 ? D / 2 : 2 * D;
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
-    const size_t at = row + r + 8 * u;
+    const uint8_t* p = rows + 8 * u * kRow;
     if constexpr (Q4) {
-      const uint8_t* p = static_cast<const uint8_t*>(c.k) + at * (D / 2) + (D / 8) * cc;
       if constexpr (D == 128) {
         const uint4 v = ld_stream16(p);
         x.w[u][0] = v.x, x.w[u][1] = v.y, x.w[u][2] = v.z, x.w[u][3] = v.w;
@@ -115,22 +113,21 @@ __device__ __forceinline__ void load_keys(KeyRegs<D, Q4>& x, const CacheArgs& c,
         const uint2 v = ld_stream8(p);
         x.w[u][0] = v.x, x.w[u][1] = v.y;
       }
-      x.pair[u] = ld_stream4(static_cast<const uint32_t*>(c.k_scale) + at);
+      x.pair[u] = ld_stream4(pairs + 32 * u);
     } else {
-      const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(c.k) + at * D + 8 * cc;
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) x.w[i][u] = ld_stream16(p + 32 * i);
+      for (int i = 0; i < D / 32; ++i) x.w[i][u] = ld_stream16(p + 64 * i);
     }
   }
 }
 
 template <int D, bool Q4>
-__device__ __forceinline__ void load_values(ValueRegs<D, Q4>& x, const CacheArgs& c, size_t row, int r, int cc) {
+__device__ __forceinline__ void load_values(ValueRegs<D, Q4>& x, const uint8_t* rows, const uint8_t* pairs) {
+  constexpr int kRow = Q4 ? D / 2 : 2 * D;
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
-    const size_t at = row + 2 * cc + (u & 1) + 8 * (u >> 1);
+    const uint8_t* p = rows + ((u & 1) + 8 * (u >> 1)) * kRow;
     if constexpr (Q4) {
-      const uint8_t* p = static_cast<const uint8_t*>(c.v) + at * (D / 2) + (D / 16) * r;
       if constexpr (D == 128) {
         const uint2 v = ld_stream8(p);
         x.w[u][0] = v.x, x.w[u][1] = v.y;
@@ -138,14 +135,13 @@ __device__ __forceinline__ void load_values(ValueRegs<D, Q4>& x, const CacheArgs
         x.w[u][0] = ld_stream4(p);
       }
     } else {
-      const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(c.v) + at * D + 8 * r;
 #pragma unroll
-      for (int i = 0; i < D / 64; ++i) x.w[u][i] = ld_stream16(p + 64 * i);
+      for (int i = 0; i < D / 64; ++i) x.w[u][i] = ld_stream16(p + 128 * i);
     }
   }
   if constexpr (Q4) {
 #pragma unroll
-    for (int u = 0; u < 2; ++u) x.pair[u] = ld_stream4(static_cast<const uint32_t*>(c.v_scale) + row + r + 8 * u);
+    for (int u = 0; u < 2; ++u) x.pair[u] = ld_stream4(pairs + 32 * u);
   }
 }
 
@@ -166,11 +162,15 @@ __device__ __forceinline__ int row_blocks(int n, int g) {
   return (int)(((long long)n * g + 8 * NR - 1) / (8 * NR));
 }
 
-// Steps of sequence b on the line.
-template <int NR>
+// A unit takes kUnitSteps + steps of the line: what starting and ending it costs, then its steps.
+// (Without the first, a piece of many short sequences took several times as long as the others.)
+template <int W>
+__host__ __device__ constexpr int unit_steps() { return 2 * W; }
+
+template <int NR, int W>
 __device__ __forceinline__ long long seq_steps(const CacheArgs& c, const AttnIn& in, int b, int step) {
   const Seq s = load_seq(c, b);
-  return (long long)c.heads * row_blocks<NR>(s.n, in.g) * steps_of(s.len, step);
+  return (long long)c.heads * row_blocks<NR>(s.n, in.g) * (steps_of(s.len, step) + unit_steps<W>());
 }
 
 }  // namespace
@@ -181,43 +181,66 @@ __host__ __device__ constexpr int partial_floats(int rows) {
   return rows * (D + 2);
 }
 
-template <int D, bool Q4, int NR>
-__global__ void __launch_bounds__(kThreads, NR == 1 ? 4 : 2)
+// 16-key blocks of a step: what a warp has in flight, against its registers.
+template <bool Q4>
+__host__ __device__ constexpr int step_blocks() { return Q4 ? 2 : 1; }
+
+// CTAs of W warps on an SM: 16 warps of 128 registers, 8 of 255 with two blocks of query rows.
+template <int NR, int W>
+__host__ __device__ constexpr int ctas_per_sm() { return (NR == 1 ? 16 : 8) / W; }
+
+template <int D, int NR, int W>
+struct DecodeShared {
+  long long line[W + 2];
+  float m[W][8 * NR], l[W][8 * NR];
+  float o[W][8 * NR][D + 4];
+};
+
+template <int D, bool Q4, int NR, int W>
+__global__ void __launch_bounds__(W * 32, ctas_per_sm<NR, W>())
     s2_cache_decode_kernel(const __grid_constant__ CacheArgs c, const __grid_constant__ AttnIn in) {
-  constexpr int kBlocks = Q4 ? 2 : 1;     // 16-key blocks of a step
+  constexpr int kThreads = W * 32;
+  constexpr int kBlocks = step_blocks<Q4>();
   constexpr int kStep = 16 * kBlocks;
   constexpr int kRows = 8 * NR;
-  constexpr int kTiles = D / 16;          // 16-channel tiles of O^T
-  __shared__ long long sh[kWarps + 2];
-  __shared__ float s_o[kWarps][kRows][D + 4];
-  __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows];
+  constexpr int kTiles = D / 16;  // 16-channel tiles of O^T
+  constexpr int kRowBytes = Q4 ? D / 2 : 2 * D;
+  extern __shared__ __align__(16) uint8_t smem[];
+  auto& sh = *reinterpret_cast<DecodeShared<D, NR, W>*>(smem);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, r = lane / 4, cc = lane % 4;
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join may start its own set-up
-  auto weight = [&](int i) { return seq_steps<NR>(c, in, i, kStep); };
-  const Line line = make_line<kThreads>(c.B, in.pieces, in.min_piece, sh, weight);
+  auto weight = [&](int i) { return seq_steps<NR, W>(c, in, i, kStep); };
+  int b;
+  long long seq_first;
+  const Line line = find_piece<kThreads>(c.B, in.pieces, in.min_piece, blockIdx.x, sh.line, weight, b, seq_first);
   const long long x0 = line.piece * blockIdx.x;
   if (x0 >= line.total) return;
   const long long x1 = min(x0 + line.piece, line.total);
-  int b;
-  long long seq_first;
-  find_seq<kThreads>(c.B, x0, sh, weight, b, seq_first);
+  // a lane's place in a block of 16 rows
+  const uint8_t* const k_base = static_cast<const uint8_t*>(c.k) + r * kRowBytes + (Q4 ? (D / 8) : 16) * cc;
+  const uint8_t* const v_base = static_cast<const uint8_t*>(c.v) + 2 * cc * kRowBytes + (Q4 ? (D / 16) : 16) * r;
+  const uint8_t* const ks_base = static_cast<const uint8_t*>(c.k_scale) + 4 * r;
+  const uint8_t* const vs_base = static_cast<const uint8_t*>(c.v_scale) + 4 * r;
 
   long long x = x0;
   while (x < x1) {
     Seq seq = load_seq(c, b);
     const int blocks = row_blocks<NR>(seq.n, in.g);
     const int steps = steps_of(seq.len, kStep);
-    if (x >= seq_first + (long long)c.heads * blocks * steps) {  // this sequence is done
-      seq_first += (long long)c.heads * blocks * steps;
+    const int span = steps + unit_steps<W>();
+    if (x >= seq_first + (long long)c.heads * blocks * span) {  // this sequence is done
+      seq_first += (long long)c.heads * blocks * span;
       ++b;
       continue;
     }
-    const long long unit = (x - seq_first) / steps;
-    const long long unit_first = seq_first + unit * steps;
+    const long long unit = (x - seq_first) / span;
+    const long long unit_first = seq_first + unit * span + unit_steps<W>();  // of its steps
     const int h = (int)(unit / blocks), rb = (int)(unit % blocks);
-    const int k0 = (int)(x - unit_first);
+    const int k0 = (int)max(0LL, x - unit_first);
     const int k1 = (int)min((long long)steps, x1 - unit_first);
+    x = unit_first + steps;
+    if (k1 <= k0) continue;
     const bool whole = k0 == 0 && k1 == steps;
 
     // ---------------------------------------------------------- query rows
@@ -285,7 +308,7 @@ __global__ void __launch_bounds__(kThreads, NR == 1 ? 4 : 2)
 
     KeyRegs<D, Q4> kr[kBlocks];
     ValueRegs<D, Q4> vr[kBlocks];
-    size_t rows[kBlocks];
+    size_t rows[kBlocks];  // first rows of the next step's blocks
     int k = k0 + warp;
     // a block behind the last key is read from the last block instead: it lies in a page of the sequence
     auto find_rows = [&](int step) {
@@ -298,13 +321,13 @@ __global__ void __launch_bounds__(kThreads, NR == 1 ? 4 : 2)
     if (seq.len > 0 && k < k1) {
       find_rows(k);
 #pragma unroll
-      for (int u = 0; u < kBlocks; ++u) load_keys(kr[u], c, rows[u], r, cc);
+      for (int u = 0; u < kBlocks; ++u) load_keys(kr[u], k_base + rows[u] * kRowBytes, ks_base + rows[u] * 4);
 #pragma unroll
-      for (int u = 0; u < kBlocks; ++u) load_values(vr[u], c, rows[u], r, cc);
-      for (; k < k1; k += kWarps) {
+      for (int u = 0; u < kBlocks; ++u) load_values(vr[u], v_base + rows[u] * kRowBytes, vs_base + rows[u] * 4);
+      for (; k < k1; k += W) {
         const int key0 = k * kStep;
-        const bool more = k + kWarps < k1;
-        if (more) find_rows(k + kWarps);
+        const bool more = k + W < k1;
+        if (more) find_rows(k + W);
         // scores: keys r, r + 8 of each block by rows 2cc, 2cc + 1
         float s[NR][kBlocks][4];
 #pragma unroll
@@ -316,10 +339,10 @@ __global__ void __launch_bounds__(kThreads, NR == 1 ? 4 : 2)
             for (int w = 0; w < D / 32; ++w)
 #pragma unroll
               for (int half = 0; half < 2; ++half) {
-                const uint32_t a0 = codes_bf16(kr[u].w[0][w] >> (4 * half));
-                const uint32_t a1 = codes_bf16(kr[u].w[1][w] >> (4 * half));
-                const uint32_t a2 = codes_bf16(kr[u].w[0][w] >> (4 * half + 8));
-                const uint32_t a3 = codes_bf16(kr[u].w[1][w] >> (4 * half + 8));
+                const uint32_t a0 = codes_128(kr[u].w[0][w] >> (4 * half));
+                const uint32_t a1 = codes_128(kr[u].w[1][w] >> (4 * half));
+                const uint32_t a2 = codes_128(kr[u].w[0][w] >> (4 * half + 8));
+                const uint32_t a3 = codes_128(kr[u].w[1][w] >> (4 * half + 8));
                 // a word's bytes 0, 2 are channels 4w, 4w + 2: qf's first pair
 #pragma unroll
                 for (int y = 0; y < NR; ++y) {
@@ -342,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, NR == 1 ? 4 : 2)
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
               const float2 pr = q4_pair(kr[u].pair[t]);
-              const float mid = fmaf(8.f, pr.x, pr.y);
+              const float mid = fmaf(-128.f, pr.x, pr.y);
 #pragma unroll
               for (int y = 0; y < NR; ++y)
 #pragma unroll
@@ -352,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, NR == 1 ? 4 : 2)
         }
         if (more) {
 #pragma unroll
-          for (int u = 0; u < kBlocks; ++u) load_keys(kr[u], c, rows[u], r, cc);
+          for (int u = 0; u < kBlocks; ++u) load_keys(kr[u], k_base + rows[u] * kRowBytes, ks_base + rows[u] * 4);
         }
         // masks, only where some row or the sequence ends in the step
         if (key0 + kStep > lim_all) {
@@ -475,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, NR == 1 ? 4 : 2)
         }
         if (more) {
 #pragma unroll
-          for (int u = 0; u < kBlocks; ++u) load_values(vr[u], c, rows[u], r, cc);
+          for (int u = 0; u < kBlocks; ++u) load_values(vr[u], v_base + rows[u] * kRowBytes, vs_base + rows[u] * 4);
         }
       }
     }
@@ -493,31 +516,31 @@ __global__ void __launch_bounds__(kThreads, NR == 1 ? 4 : 2)
         const int row = y * 8 + 2 * cc + e;
 #pragma unroll
         for (int j = 0; j < kTiles; ++j) {
-          s_o[warp][row][channel_of<D, Q4>(j, false, r)] = acc[y][j][e] + vsum[y][e];
-          s_o[warp][row][channel_of<D, Q4>(j, true, r)] = acc[y][j][2 + e] + vsum[y][e];
+          sh.o[warp][row][channel_of<D, Q4>(j, false, r)] = acc[y][j][e] + vsum[y][e];
+          sh.o[warp][row][channel_of<D, Q4>(j, true, r)] = acc[y][j][2 + e] + vsum[y][e];
         }
         if (r == 0) {
-          s_m[warp][row] = m[y][e];
-          s_l[warp][row] = l[y][e];
+          sh.m[warp][row] = m[y][e];
+          sh.l[warp][row] = l[y][e];
         }
       }
     __syncthreads();
     // four channels of a row a thread; rows of no token are left out
     const int rows_here = min(kRows, seq.n * in.g - rb * kRows);
-    float* part = in.partial + (size_t)(2 * blockIdx.x + (x == x0 ? 0 : 1)) * partial_floats<D>(kRows);
+    float* part = in.partial + (size_t)(2 * blockIdx.x + (unit_first < x0 ? 0 : 1)) * partial_floats<D>(kRows);
     for (int i = threadIdx.x; i < rows_here * (D / 4); i += kThreads) {
       const int row = i / (D / 4), d = 4 * (i % (D / 4));
-      float mm = s_m[0][row];
+      float mm = sh.m[0][row];
 #pragma unroll
-      for (int w = 1; w < kWarps; ++w) mm = fmaxf(mm, s_m[w][row]);
+      for (int w = 1; w < W; ++w) mm = fmaxf(mm, sh.m[w][row]);
       float ll = 0.f;
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        if (s_m[w][row] == -INFINITY) continue;
-        const float f = ex2(s_m[w][row] - mm);
-        const float4 v = *reinterpret_cast<const float4*>(&s_o[w][row][d]);
-        ll += s_l[w][row] * f;
+      for (int w = 0; w < W; ++w) {
+        if (sh.m[w][row] == -INFINITY) continue;
+        const float f = ex2(sh.m[w][row] - mm);
+        const float4 v = *reinterpret_cast<const float4*>(&sh.o[w][row][d]);
+        ll += sh.l[w][row] * f;
         o.x += v.x * f, o.y += v.y * f, o.z += v.z * f, o.w += v.w * f;
       }
       if (whole) {
@@ -536,42 +559,41 @@ __global__ void __launch_bounds__(kThreads, NR == 1 ? 4 : 2)
       }
     }
     __syncthreads();
-    x = unit_first + k1;
   }
 }
 
 // Joins the partial sums of units that the line's cuts run through.  CTA i
 // stands for cut i + 1; the CTAs of one unit's cuts share its rows and
 // channels out among them.  The order of the sum is the pieces'.
-template <int D, bool Q4, int NR>
-__global__ void __launch_bounds__(kThreads) s2_cache_join_kernel(const __grid_constant__ CacheArgs c,
-                                                                 const __grid_constant__ AttnIn in) {
-  constexpr int kStep = Q4 ? 32 : 16;
+template <int D, bool Q4, int NR, int W>
+__global__ void __launch_bounds__(128) s2_cache_join_kernel(const __grid_constant__ CacheArgs c,
+                                                            const __grid_constant__ AttnIn in) {
+  constexpr int kThreads = 128, kWarps = kThreads / 32;
+  constexpr int kStep = 16 * step_blocks<Q4>();
   constexpr int kRows = 8 * NR;
   constexpr int kGroups = kThreads / 8;  // partial sums added side by side, 8 lanes of 4 channels each
   __shared__ long long sh[kWarps + 2];
   __shared__ float s_red[2][kWarps];
   __shared__ float4 s_o[kGroups][8];
-  auto weight = [&](int i) { return seq_steps<NR>(c, in, i, kStep); };
-  const Line line = make_line<kThreads>(c.B, in.pieces, in.min_piece, sh, weight);
-  const long long cut = line.piece * (blockIdx.x + 1);
-  if (cut >= line.total) return;
+  auto weight = [&](int i) { return seq_steps<NR, W>(c, in, i, kStep); };
   int b;
   long long seq_first;
-  find_seq<kThreads>(c.B, cut, sh, weight, b, seq_first);
+  const Line line = find_piece<kThreads>(c.B, in.pieces, in.min_piece, blockIdx.x + 1, sh, weight, b, seq_first);
+  const long long cut = line.piece * (blockIdx.x + 1);
+  if (cut >= line.total) return;
   const Seq seq = load_seq(c, b);
-  const int steps = steps_of(seq.len, kStep), blocks = row_blocks<NR>(seq.n, in.g);
-  const long long unit = (cut - seq_first) / steps;
-  const long long first = seq_first + unit * steps, last = first + steps - 1;
-  if (first == cut) return;  // the cut lies between two units
-  const int p0 = (int)(first / line.piece), p1 = (int)(last / line.piece);  // pieces that hold the unit
+  const int steps = steps_of(seq.len, kStep), blocks = row_blocks<NR>(seq.n, in.g), span = steps + unit_steps<W>();
+  const long long unit = (cut - seq_first) / span;
+  const long long first = seq_first + unit * span + unit_steps<W>(), last = first + steps - 1;  // of its steps
+  if (cut <= first) return;  // the cut lies before the unit's first step
+  const int p0 = (int)(first / line.piece), p1 = (int)(last / line.piece);  // pieces that hold its steps
   const int nth = (int)blockIdx.x - p0, helpers = p1 - p0;
   const int h = (int)(unit / blocks), rb = (int)(unit % blocks);
   const int rows_here = min(kRows, seq.n * in.g - rb * kRows);
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  // piece p holds the unit as its first when the unit begins at or before the piece
+  // a piece's first partial unit is one that began before it
   auto part_of = [&](int p) -> const float* {
-    const int slot = 2 * p + (first <= line.piece * p ? 0 : 1);
+    const int slot = 2 * p + (first < line.piece * p ? 0 : 1);
     return in.partial + (size_t)slot * partial_floats<D>(kRows);
   };
   const int group = threadIdx.x / 8, e = threadIdx.x % 8, lane = threadIdx.x % 32, warp = threadIdx.x / 32;
@@ -626,26 +648,35 @@ __global__ void __launch_bounds__(kThreads) s2_cache_join_kernel(const __grid_co
   }
 }
 
-template <int D, bool Q4, int NR>
-static int decode_impl(const CacheArgs& c, const AttnIn& in, cudaStream_t stream) {
-  s2_cache_decode_kernel<D, Q4, NR><<<kDecodePieces, kThreads, 0, stream>>>(c, in);
-  cudaError_t e = cudaGetLastError();
+template <int D, bool Q4, int NR, int W>
+static int decode_impl(const CacheArgs& c, const AttnIn& in0, cudaStream_t stream) {
+  AttnIn in = in0;
+  in.pieces = 148 * ctas_per_sm<NR, W>();
+  in.min_piece = unit_steps<W>() + W;  // a step for each warp
+  constexpr int kBytes = (int)sizeof(DecodeShared<D, NR, W>);
+  cudaError_t e;
+  if (kBytes > 48 * 1024) {
+    e = cudaFuncSetAttribute(s2_cache_decode_kernel<D, Q4, NR, W>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
+    if (e != cudaSuccess) return (int)e;
+  }
+  s2_cache_decode_kernel<D, Q4, NR, W><<<in.pieces, W * 32, kBytes, stream>>>(c, in);
+  e = cudaGetLastError();
   if (e != cudaSuccess) return (int)e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(kDecodePieces - 1);
-  cfg.blockDim = dim3(kThreads);
+  cfg.gridDim = dim3(in.pieces - 1);
+  cfg.blockDim = dim3(128);
   cfg.stream = stream;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return (int)cudaLaunchKernelEx(&cfg, s2_cache_join_kernel<D, Q4, NR>, c, in);
+  return (int)cudaLaunchKernelEx(&cfg, s2_cache_join_kernel<D, Q4, NR, W>, c, in);
 }
 
 template <int D, bool Q4>
 static int decode_rows(const CacheArgs& c, const AttnIn& in, int rows, cudaStream_t stream) {
-  return rows <= 8 ? decode_impl<D, Q4, 1>(c, in, stream) : decode_impl<D, Q4, 2>(c, in, stream);
+  return rows <= 8 ? decode_impl<D, Q4, 1, 4>(c, in, stream) : decode_impl<D, Q4, 2, 4>(c, in, stream);
 }
 
 int launch_cache_decode(const CacheArgs& c, const AttnIn& in, int D, bool q4, int rows, cudaStream_t stream) {

@@ -87,7 +87,7 @@ class Paged:
         ck, cv = split_codes(take(self.k)), split_codes(take(self.v))
         ks, vs = take(self.ks).double(), take(self.vs).double()
         k, v = ks[:, 1:] + ks[:, :1] * ck, vs[:, 1:] + vs[:, :1] * cv
-        return (k, v, ks[:, :1].abs() * (ck - 8).abs() + (ks[:, 1:] + 8 * ks[:, :1]).abs(),
+        return (k, v, ks[:, :1].abs() * (128 + ck) + (ks[:, 1:] - 128 * ks[:, :1]).abs(),
                 vs[:, :1].abs() * (cv - 8).abs())
 
 
@@ -95,8 +95,9 @@ def attention(cache, q, starts):
     """o [T, H, D], lse [T, H] in 64 bits of the new tokens q [T, H, D] (starts: packed starts of the new tokens), and
     the errors that the kernels may make of each.
 
-    Scores: products of bf16 values (4 bits: whole numbers times bf16) are exact in 32 bits; a sum of D of them and the
-    scaling are off by at most (D + 8) roundings of the terms' absolute sum.  Weights: twice that, relatively, and
+    Scores: products of bf16 values are exact in 32 bits; a sum of D of them and the scaling are off by at most (D + 8)
+    roundings of the terms' absolute sum.  The terms of 4-bit rows are q·scale·(128 + code) and q·(min - 128 scale): bf16
+    holds 128 + code as it is, and the two sums are taken one from the other.  Weights: twice that, relatively, and
     2^-21 of the exponential.  o: each weight is rounded to bf16 before the product (U of its term), the sums over n
     keys by n F, and the result once to bf16.  lse: the scores' error, the sum's, and a few roundings of itself."""
     T, H, D = q.shape
