@@ -21,6 +21,9 @@ import torch
 from . import binding
 from .binding import _check, _ptr, lib
 
+# the current stream's handle without the object around it: a step's calls are short enough for that to count
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
 CACHE_BF16, CACHE_Q4 = 0, 1
 
 
@@ -101,16 +104,22 @@ class CacheBatch:
         self.address = ctypes.addressof(self._struct)
 
 
+def _stream(stream, cache) -> int:
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(cache.device.index)
+    return binding._stream(stream)
+
+
 # ------------------------------------------------------------------ raw entry points (same names as the C ABI)
 
 
 def s2attn_cache_append(cache, batch, q, ldq, k, ldk, v, ldv, q_out, heads, positions, base, scale, stream=None) -> int:
     return lib().s2attn_cache_append(cache.address, batch.address, _ptr(q), ldq, _ptr(k), ldk, _ptr(v), ldv,
-                                     _ptr(q_out), heads, _ptr(positions), base, scale, binding._stream(stream))
+                                     _ptr(q_out), heads, _ptr(positions), base, scale, _stream(stream, cache))
 
 
 def s2attn_cache_read(cache, batch, k_out, v_out, stream=None) -> int:
-    return lib().s2attn_cache_read(cache.address, batch.address, _ptr(k_out), _ptr(v_out), binding._stream(stream))
+    return lib().s2attn_cache_read(cache.address, batch.address, _ptr(k_out), _ptr(v_out), _stream(stream, cache))
 
 
 def s2attn_cache_attn_workspace_size(cache, batch, heads) -> int:
@@ -119,7 +128,7 @@ def s2attn_cache_attn_workspace_size(cache, batch, heads) -> int:
 
 def s2attn_cache_attn(cache, batch, q, ldq, o, lse, heads, workspace, workspace_bytes, stream=None) -> int:
     return lib().s2attn_cache_attn(cache.address, batch.address, _ptr(q), ldq, _ptr(o), _ptr(lse), heads,
-                                   _ptr(workspace), workspace_bytes, binding._stream(stream))
+                                   _ptr(workspace), workspace_bytes, _stream(stream, cache))
 
 
 # ------------------------------------------------------------------ tensor-level helpers
@@ -142,17 +151,21 @@ def _plain(cache, stream):
     return stream is None and cache.device.index == torch.cuda.current_device()
 
 
-def _rows(name, t, cache, batch, heads=None):
+def _rows(name, t, cache, batch, heads):
     """Row stride of [tokens, heads, D] bf16 rows whose heads lie side by side."""
-    if t.dim() != 3 or t.dtype != torch.bfloat16 or t.device != cache.device:
-        raise ValueError("%s must be bf16 [tokens, heads, D] on the cache's device" % name)
-    T, H, D = t.shape
-    if T != batch.tokens or D != cache.dim or (heads is not None and H != heads):
-        raise ValueError("%s is %s for %d tokens and rows of %d" % (name, tuple(t.shape), batch.tokens, cache.dim))
-    st = t.stride()
-    if st[2] != 1 or (H > 1 and st[1] != D):
+    if t.dtype != torch.bfloat16 or t.device != cache.device or t.shape != (batch.tokens, heads, cache.dim):
+        raise ValueError("%s must be bf16 [%d, %d, %d] on the cache's device" % (
+            name, batch.tokens, heads, cache.dim))
+    row, head, one = t.stride()
+    if one != 1 or (heads > 1 and head != cache.dim):
         raise ValueError("the heads of a token of %s must lie side by side" % name)
-    return st[0] if T > 1 else max(st[0], H * D)
+    return row if batch.tokens > 1 else max(row, heads * cache.dim)
+
+
+def _query_heads(q):
+    if q.dim() != 3:
+        raise ValueError("q must be bf16 [tokens, heads, D]")
+    return q.shape[1]
 
 
 def _same_device(cache, batch):
@@ -176,7 +189,8 @@ def cache_append(cache: KVCache, batch: CacheBatch, k, v, q=None, positions=None
     ldk, ldv = _rows("k", k, cache, batch, cache.heads), _rows("v", v, cache, batch, cache.heads)
     ldq = heads = 0
     if q is not None:
-        ldq, heads = _rows("q", q, cache, batch), q.shape[1]
+        heads = _query_heads(q)
+        ldq = _rows("q", q, cache, batch, heads)
         if out is None:
             out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
         else:
@@ -223,7 +237,8 @@ def cache_attention(cache: KVCache, batch: CacheBatch, q, out=None, lse=None, wo
         with _on(cache.device, stream):
             return cache_attention(cache, batch, q, out, lse, workspace)
     _same_device(cache, batch)
-    ldq, heads = _rows("q", q, cache, batch), q.shape[1]
+    heads = _query_heads(q)
+    ldq = _rows("q", q, cache, batch, heads)
     if out is None:
         out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
     else:

@@ -96,6 +96,15 @@ __device__ __forceinline__ uint4 pack8(const float* x) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// min(rint(a / s), 15): by the reciprocal, whose product is within 1e-5 of the quotient, and by the division where
+// that could round the other way (or where s has no reciprocal).
+__device__ __forceinline__ uint32_t code_of(float a, float s, float inv) {
+  const float y = a * inv;
+  float n = rintf(y);
+  if (!(fabsf(fabsf(y - n) - 0.5f) > 1e-4f) || s < 1e-30f) n = rintf(__fdiv_rn(a, s));
+  return (uint32_t)fminf(n, 15.f);
+}
+
 // Packs a row held by LANES lanes (bf16 values) to 4 bits: this lane's 8 bytes and the row's (scale, min).
 // A row with a NaN or an infinity reads back as NaN.
 template <int LANES>
@@ -122,12 +131,9 @@ __device__ __forceinline__ void pack_row(const Row& x, uint2& codes, uint32_t& p
   const float s = __bfloat162float(sb);
   uint32_t w[2] = {0u, 0u};
   if (good && s > 0.f) {
+    const float inv = 1.0f / s;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float lo = fminf(rintf(__fdiv_rn(x.lo[i] - mn, s)), 15.f);
-      const float hi = fminf(rintf(__fdiv_rn(x.hi[i] - mn, s)), 15.f);
-      w[i / 4] |= ((uint32_t)lo | ((uint32_t)hi << 4)) << (8 * (i % 4));
-    }
+    for (int i = 0; i < 8; ++i) w[i / 4] |= (code_of(x.lo[i] - mn, s, inv) | (code_of(x.hi[i] - mn, s, inv) << 4)) << (8 * (i % 4));
   }
   if (!good) sb = mb = __float2bfloat16_rn(NAN);
   codes = make_uint2(w[0], w[1]);
@@ -136,14 +142,45 @@ __device__ __forceinline__ void pack_row(const Row& x, uint2& codes, uint32_t& p
 
 }  // namespace
 
-// Rows of a token in order: H query heads (none without q), Hkv key heads, Hkv value heads.
+// A thread's way through the rows of the CTA's tokens: row `r` of token `x`, kRows further each time.
+struct RowAt {
+  int x, r;
+  __device__ __forceinline__ void next(int by, int per_token) {
+    r += by;
+    while (r >= per_token) {
+      r -= per_token;
+      ++x;
+    }
+  }
+};
+
+// Rows of a token in order: H query heads (none without q), Hkv key heads, Hkv value heads.  Where a row
+// comes from does not depend on its sequence: the first rows are on their way before the tokens are found,
+// and each next row while the last one is worked on.
 template <int D, bool Q4, bool kRotate>
 __global__ void __launch_bounds__(kThreads) s2_cache_append_kernel(const __grid_constant__ CacheArgs c,
                                                                    const __grid_constant__ AppendIn in) {
   constexpr int kHalf = D / 2, kLanes = D / 16, kRows = kThreads / kLanes;
   __shared__ Token tok[kTok];
-  __shared__ float2 cs[kTok][kHalf];
+  __shared__ __align__(16) float2 cs[kTok][kHalf];
   const int t0 = blockIdx.x * kTok;
+  const int here = min(kTok, c.T - t0);
+  const int per_token = in.q_heads + 2 * c.heads;
+  const int lane = threadIdx.x % kLanes;
+  RowAt at{0, 0};
+  at.next(threadIdx.x / kLanes, per_token);
+  uint4 lo = make_uint4(0u, 0u, 0u, 0u), hi = lo;
+  auto load = [&](const RowAt& a) {
+    if (a.x >= here) return;
+    const int v0 = in.q_heads + c.heads;
+    const __nv_bfloat16* src = (a.r < in.q_heads ? in.q + (size_t)(t0 + a.x) * in.ldq + (size_t)a.r * D
+                                : a.r < v0       ? in.k + (size_t)(t0 + a.x) * in.ldk + (size_t)(a.r - in.q_heads) * D
+                                                 : in.v + (size_t)(t0 + a.x) * in.ldv + (size_t)(a.r - v0) * D) +
+                               8 * lane;
+    lo = *reinterpret_cast<const uint4*>(src);
+    hi = *reinterpret_cast<const uint4*>(src + kHalf);
+  };
+  load(at);
   find_tokens(c, t0, tok);
   __syncthreads();
   if constexpr (kRotate) {
@@ -159,59 +196,50 @@ __global__ void __launch_bounds__(kThreads) s2_cache_append_kernel(const __grid_
     }
     __syncthreads();
   }
-  const int per_token = in.q_heads + 2 * c.heads;
-  const int lane = threadIdx.x % kLanes;
-  const int total = kTok * per_token;
   // whole warps go around together (the packing's shuffles need all lanes)
-  for (int w0 = 0; w0 < total; w0 += kRows) {
-    const int w = w0 + threadIdx.x / kLanes;
-    const int x = w / per_token, r = w % per_token;
-    const bool is_q = r < in.q_heads, is_v = r >= in.q_heads + c.heads;
-    const int h = is_q ? r : is_v ? r - in.q_heads - c.heads : r - in.q_heads;
-    const bool live = w < total && (is_q ? tok[x].mine : tok[x].store);
+  for (int w0 = 0; w0 < here * per_token; w0 += kRows) {
+    const RowAt now = at;
     Row row;
-    if (live) {
-      const __nv_bfloat16* src = (is_q ? in.q + (size_t)(t0 + x) * in.ldq
-                                  : is_v ? in.v + (size_t)(t0 + x) * in.ldv
-                                         : in.k + (size_t)(t0 + x) * in.ldk) + (size_t)h * D + 8 * lane;
-      unpack8(*reinterpret_cast<const uint4*>(src), row.lo);
-      unpack8(*reinterpret_cast<const uint4*>(src + kHalf), row.hi);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) row.lo[i] = row.hi[i] = 0.f;
-    }
+    unpack8(lo, row.lo);
+    unpack8(hi, row.hi);
+    at.next(kRows, per_token);
+    load(at);
+    const bool is_q = now.r < in.q_heads, is_v = now.r >= in.q_heads + c.heads;
+    const int h = is_q ? now.r : is_v ? now.r - in.q_heads - c.heads : now.r - in.q_heads;
+    const bool live = now.x < here && (is_q ? tok[now.x].mine : tok[now.x].store);
     if (kRotate && live && !is_v) {
+      const float4* angles = reinterpret_cast<const float4*>(&cs[now.x][8 * lane]);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float2 a = cs[x][8 * lane + i];
+        const float4 a4 = angles[i / 2];
+        const float co = i % 2 ? a4.z : a4.x, si = i % 2 ? a4.w : a4.y;
         // products rounded one by one, as plain 32-bit arithmetic does it: a value at a rounding border
         // must not depend on the compiler's choice, since 4-bit codes are made from it
-        const float lo = __fsub_rn(__fmul_rn(row.lo[i], a.x), __fmul_rn(row.hi[i], a.y));
-        const float hi = __fadd_rn(__fmul_rn(row.hi[i], a.x), __fmul_rn(row.lo[i], a.y));
-        row.lo[i] = lo;
-        row.hi[i] = hi;
+        const float a = __fsub_rn(__fmul_rn(row.lo[i], co), __fmul_rn(row.hi[i], si));
+        const float b = __fadd_rn(__fmul_rn(row.hi[i], co), __fmul_rn(row.lo[i], si));
+        row.lo[i] = a;
+        row.hi[i] = b;
       }
     }
-    const uint4 lo = pack8(row.lo), hi = pack8(row.hi);
-    if (!Q4 || is_q) {
-      if (live) {
-        __nv_bfloat16* dst = is_q ? in.q_out + ((size_t)(t0 + x) * in.q_heads + h) * D
-                                  : static_cast<__nv_bfloat16*>(is_v ? c.v : c.k) +
-                                        row_of(c, tok[x].page, h, tok[x].place) * D;
-        *reinterpret_cast<uint4*>(dst + 8 * lane) = lo;
-        *reinterpret_cast<uint4*>(dst + kHalf + 8 * lane) = hi;
-      }
+    const uint4 out_lo = pack8(row.lo), out_hi = pack8(row.hi);
+    if (live && (!Q4 || is_q)) {
+      __nv_bfloat16* dst = is_q ? in.q_out + ((size_t)(t0 + now.x) * in.q_heads + h) * D
+                                : static_cast<__nv_bfloat16*>(is_v ? c.v : c.k) +
+                                      row_of(c, tok[now.x].page, h, tok[now.x].place) * D;
+      *reinterpret_cast<uint4*>(dst + 8 * lane) = out_lo;
+      *reinterpret_cast<uint4*>(dst + kHalf + 8 * lane) = out_hi;
     }
     if constexpr (Q4) {
-      unpack8(lo, row.lo);  // the row as bf16 holds it
-      unpack8(hi, row.hi);
+      if (!__any_sync(0xffffffffu, live && !is_q)) continue;
+      unpack8(out_lo, row.lo);  // the row as bf16 holds it
+      unpack8(out_hi, row.hi);
       uint2 codes;
       uint32_t pair;
       pack_row<kLanes>(row, codes, pair);
       if (live && !is_q) {
-        const size_t at = row_of(c, tok[x].page, h, tok[x].place);
-        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(is_v ? c.v : c.k) + at * kHalf + 8 * lane) = codes;
-        if (lane == 0) static_cast<uint32_t*>(is_v ? c.v_scale : c.k_scale)[at] = pair;
+        const size_t to = row_of(c, tok[now.x].page, h, tok[now.x].place);
+        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(is_v ? c.v : c.k) + to * kHalf + 8 * lane) = codes;
+        if (lane == 0) static_cast<uint32_t*>(is_v ? c.v_scale : c.k_scale)[to] = pair;
       }
     }
   }
@@ -230,6 +258,7 @@ __global__ void __launch_bounds__(kThreads) s2_cache_read_kernel(const __grid_co
   __syncthreads();
   const int per_token = 2 * c.heads;
   const int lane = threadIdx.x % kLanes;
+#pragma unroll 2
   for (int w = threadIdx.x / kLanes; w < kTok * per_token; w += kRows) {
     const int x = w / per_token, r = w % per_token;
     if (!tok[x].store) continue;

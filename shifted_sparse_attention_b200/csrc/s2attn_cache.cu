@@ -137,8 +137,16 @@ int s2attn_cache_append(const s2_cache* cache, const s2_cache_batch* batch, cons
   in.ldk = ldk;
   in.ldv = ldv;
   in.q_heads = q ? (int)heads : 0;
-  for (int j = 0; j < 64; ++j)
-    in.turns[j] = rotate && j < D / 2 ? scale * std::pow(base, -2.0 * j / (double)D) / 6.283185307179586477 : 0.0;
+  // a program's calls all have one base and scale: the thread's last table serves them
+  thread_local struct { double base, scale; int64_t D; double turns[64]; } last = {0.0, 0.0, 0, {}};
+  if (rotate && (last.base != base || last.scale != scale || last.D != D)) {
+    for (int j = 0; j < (int)D / 2; ++j)
+      last.turns[j] = scale * std::pow(base, -2.0 * j / (double)D) / 6.283185307179586477;
+    last.base = base;
+    last.scale = scale;
+    last.D = D;
+  }
+  for (int j = 0; j < 64; ++j) in.turns[j] = last.turns[j];
   return launched(s2::launch_cache_append(a, in, (int)D, cache->format == S2_CACHE_Q4, rotate,
                                           static_cast<cudaStream_t>(stream)),
                   "cache append");
