@@ -21,10 +21,12 @@
 // the softmax are those of s2_fwd.cu: S and P share columns, P feeds O += P V
 // from TMEM, and the running maximum moves in steps of 8 (in powers of two).
 //
-// 4 bits: tiles hold codes - 8 (whole numbers, exact in bf16).  The softmax
-// applies scale and min of each key: s = sk (q·c') + (mk + 8 sk) sum(q); the
-// weight that goes into the product is p·sv (rounded to bf16, relative 2^-9),
-// and sum p (mv + 8 sv), the same for every channel, is kept beside O.
+// 4 bits: packed rows come by bulk copies and are unpacked to whole numbers
+// that bf16 holds as they are, 128 + code for keys (no subtraction) and code - 8
+// for values (so that rounded weights meet small numbers).  The softmax applies
+// scale and min of each key: s = sk (q·k') + (mk - 128 sk) sum(q); the weight that
+// goes into the product is p·sv (rounded to bf16, relative 2^-9), and
+// sum p (mv + 8 sv), the same for every channel, is kept beside O.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -40,13 +42,14 @@ namespace chunk {
 constexpr int kT = 128;  // rows of a tile, of queries and of keys
 constexpr int kChunkBytes = kT * 128;
 constexpr int kSegs = 48;          // units (or parts) that a CTA looks ahead
-constexpr int kScaleSlots = 4;
+constexpr int kScaleSlots = 2;
+constexpr int kRawSlots = 3;       // key tiles of packed rows in flight (4-bit pages)
 constexpr long long kUnitKeys = 256;  // what starting and ending a unit costs, in keys
 
 template <bool Q4>
 __host__ __device__ constexpr int threads() { return Q4 ? 384 : 320; }
 template <bool Q4>
-__host__ __device__ constexpr int slots() { return Q4 ? 4 : 5; }
+__host__ __device__ constexpr int slots() { return Q4 ? 3 : 5; }
 
 enum Bar {
   KV_FULL = 0,                          // + slot (5)
@@ -58,9 +61,11 @@ enum Bar {
   Q_EMPTY = 17,
   TAIL = 18,                            // the last value tile of a sequence, before its unused rows are zeroed
   MMA_DONE = 19,
-  SC_FULL = 20,                         // + scale slot (4)
-  SC_EMPTY = 24,                        // + scale slot (4)
-  NUM_BARS = 28
+  SC_FULL = 20,                         // + scale slot (2)
+  SC_EMPTY = 22,                        // + scale slot (2)
+  RAW_FULL = 24,                        // + raw slot (3)
+  RAW_EMPTY = 27,                       // + raw slot (3)
+  NUM_BARS = 30
 };
 
 // Part of a unit that a CTA computes.
@@ -88,7 +93,10 @@ struct Layout {
   static constexpr int kQ = 0;
   static constexpr int kKV = 2 * kQBytes;
   static constexpr int kScale = kKV + slots<Q4>() * kKVBytes;  // per slot {sk, mk'} of the keys, then {sv, mv'}
-  static constexpr int kBars = kScale + (Q4 ? kScaleSlots * kT * 16 : 0);
+  // packed rows of a key tile: key codes, value codes, key pairs, value pairs
+  static constexpr int kRaw = kScale + (Q4 ? kScaleSlots * kT * 16 : 0);
+  static constexpr int kRawBytes = kT * (D + 8);
+  static constexpr int kBars = kRaw + (Q4 ? kRawSlots * kRawBytes : 0);
   static constexpr int kMisc = kBars + NUM_BARS * 8;
   static constexpr int kLine = kMisc + 16;  // make_line's and find_seq's sums
   static constexpr int kWalk = kLine + 18 * 8;
@@ -134,9 +142,9 @@ __device__ __forceinline__ int pair_tiles(const Seq& s, const Units& u, int j) {
   const int first = j * u.d;
   return last_tile(s.len - s.n + first, min(u.d, s.n - first)) + 1;
 }
-// Key tiles of a unit that lie before point w of its weight.
+// Key tiles of a unit that lie before point w of its weight (the same for all that ask, and growing with w).
 __device__ __forceinline__ int tile_at(int tiles, long long w, long long weight) {
-  return w >= weight ? tiles : (int)(w * tiles / weight);
+  return w >= weight ? tiles : min(tiles, __double2int_rd(__ddiv_rn((double)w * tiles, (double)weight)));
 }
 
 // The next segments of a CTA's piece (one thread); returns their number.
@@ -179,14 +187,22 @@ __device__ __noinline__ int walk_on(Walk& w, const CacheArgs& c, int per_tile, S
   return k;
 }
 
-// The clobber keeps these loads where they stand: moved up together they would fill the registers.
-__device__ __forceinline__ float4 ld_shared_f4(uint32_t at) {
-  float4 v;
-  asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(at)
-               : "memory");
-  return v;
+// {scale, min} of eight keys, the same for all lanes: four loads at once, so that their wait is shared.
+// The clobber keeps them where they stand: moved up together they would fill the registers.
+struct Pairs8 {
+  float4 p[4];
+};
+__device__ __forceinline__ void load_pairs(Pairs8& v, uint32_t at) {
+  asm volatile(
+      "ld.shared.v4.f32 {%0,%1,%2,%3}, [%16];\n\t"
+      "ld.shared.v4.f32 {%4,%5,%6,%7}, [%16+16];\n\t"
+      "ld.shared.v4.f32 {%8,%9,%10,%11}, [%16+32];\n\t"
+      "ld.shared.v4.f32 {%12,%13,%14,%15}, [%16+48];"
+      : "=f"(v.p[0].x), "=f"(v.p[0].y), "=f"(v.p[0].z), "=f"(v.p[0].w), "=f"(v.p[1].x), "=f"(v.p[1].y),
+        "=f"(v.p[1].z), "=f"(v.p[1].w), "=f"(v.p[2].x), "=f"(v.p[2].y), "=f"(v.p[2].z), "=f"(v.p[2].w),
+        "=f"(v.p[3].x), "=f"(v.p[3].y), "=f"(v.p[3].z), "=f"(v.p[3].w)
+      : "r"(at)
+      : "memory");
 }
 
 }  // namespace chunk
@@ -240,6 +256,10 @@ __global__ void __launch_bounds__(chunk::threads<Q4>(), 1)
       mbar_init(bar(SC_FULL + i), 64);
       mbar_init(bar(SC_EMPTY + i), 256);
     }
+    for (int i = 0; i < kRawSlots; ++i) {
+      mbar_init(bar(RAW_FULL + i), 1);
+      mbar_init(bar(RAW_EMPTY + i), 64);
+    }
     *abort_flag = 0;
     fence_barrier_init();
     fence_proxy_async_smem();
@@ -253,11 +273,10 @@ __global__ void __launch_bounds__(chunk::threads<Q4>(), 1)
     const Seq s = load_seq(c, b);
     return s.n > 0 ? Units(s, per_tile).head() * c.heads : 0;
   };
-  const Line line = make_line<kThreads>(c.B, in.pieces, in.min_piece, line_sh, weight_of);
+  int b_first;
+  long long b_start;
+  const Line line = find_piece<kThreads>(c.B, in.pieces, in.min_piece, blockIdx.x, line_sh, weight_of, b_first, b_start);
   const long long x0 = line.piece * blockIdx.x, x1 = min(x0 + line.piece, line.total);
-  int b_first = -1;
-  long long b_start = 0;
-  if (x0 < x1) find_seq<kThreads>(c.B, x0, line_sh, weight_of, b_first, b_start);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -278,327 +297,447 @@ __global__ void __launch_bounds__(chunk::threads<Q4>(), 1)
     }
   }
 
-  // Counters that run on from segment to segment (each role keeps those it uses).
-  int e = 0;                  // key and value tiles so far: e-th goes to slot e % kSlots
-  int n_seg = 0;              // segments with keys
-  int nA = 0, nB = 0;         // key tiles of each query tile
-  int oA = 0, oB = 0;         // segments in which each query tile had keys
-  int n_sc = 0;               // key tiles (scale slots)
-  int n_tail = 0;
+  // All roles walk the same list of segments; thread 0 writes it, in pieces.  Counters of barrier phases run on
+  // from segment to segment, and each role keeps its own, so that the softmax's registers hold nothing else's.
   bool ok = true;
-
-  while (true) {
-    // ------------------------------------------------------------ the next segments
+  auto next_list = [&]() -> int {
+    __syncthreads();  // everyone is done with the last list
     if (threadIdx.x == 0) *count = *abort_flag ? 0 : walk_on(*walk, c, per_tile, segs, kList);
     __syncthreads();
-    const int k_segs = *count;
-    if (k_segs == 0) break;
+    return *count;
+  };
+#define FOR_SEGMENTS                                        \
+  for (int k_segs = next_list(); k_segs > 0; k_segs = next_list()) \
+    for (int si = 0; si < k_segs && ok; ++si)
+// Tokens of the segment's two query tiles, the last key tile of each (or -1), and whether they have keys here.
+#define SEGMENT_OF(g)                                                                   \
+  const int cntA = min(g.left, per_tile), cntB = min(g.left - per_tile, per_tile);      \
+  const int lastA = min(last_tile(g.place, cntA), g.t1 - 1);                            \
+  const int lastB = min(last_tile(g.place + per_tile, cntB), g.t1 - 1);                 \
+  const bool hasA = lastA >= g.t0, hasB = lastB >= g.t0, keys = g.t1 > g.t0;
 
-    for (int si = 0; si < k_segs && ok; ++si) {
+  if (warp == 8) {
+    // ------------------------------------------------------------ TMA
+    int e = 0;       // key and value tiles so far: the e-th goes to slot e % kSlots
+    int n_seg = 0;   // segments with keys
+    int n_tail = 0;
+    int n_raw = 0;   // key tiles of packed rows
+    FOR_SEGMENTS {
       const Seg g = segs[si];
-      const int cntA = min(g.left, per_tile), cntB = min(g.left - per_tile, per_tile);
-      const int lastA = min(last_tile(g.place, cntA), g.t1 - 1);
-      const int lastB = min(last_tile(g.place + per_tile, cntB), g.t1 - 1);
-      const bool hasA = lastA >= g.t0, hasB = lastB >= g.t0;
-      const bool keys = g.t1 > g.t0;
-
-      if (warp == 8) {
-        // -------------------------------------------------------- TMA
-        if (!keys) continue;
-        if (lane == 0) {
-          if (n_seg > 0) ok = s2_wait(bar(Q_EMPTY), (n_seg - 1) & 1, abort_flag, status, 1);
-          if (ok) {
-            const uint32_t bytes = (uint32_t)(per_tile * in.g) * 128 * kChunks;
-            mbar_arrive_expect_tx(bar(Q_FULL), (hasA ? bytes : 0) + (hasB ? bytes : 0));
+      SEGMENT_OF(g)
+      if (!keys) continue;
+      if (lane == 0) {
+        if (n_seg > 0) ok = s2_wait(bar(Q_EMPTY), (n_seg - 1) & 1, abort_flag, status, 1);
+        if (ok) {
+          const uint32_t bytes = (uint32_t)(per_tile * in.g) * 128 * kChunks;
+          mbar_arrive_expect_tx(bar(Q_FULL), (hasA ? bytes : 0) + (hasB ? bytes : 0));
 #pragma unroll
-            for (int x = 0; x < 2; ++x)
-              if (x ? hasB : hasA)
-                for (int ch = 0; ch < kChunks; ++ch)
-                  tma_load_3d(sQ(x) + ch * kChunkBytes, &tmQ, ch * 64, g.h * in.g, g.tok + x * per_tile, bar(Q_FULL));
-          }
+          for (int x = 0; x < 2; ++x)
+            if (x ? hasB : hasA)
+              for (int ch = 0; ch < kChunks; ++ch)
+                tma_load_3d(sQ(x) + ch * kChunkBytes, &tmQ, ch * 64, g.h * in.g, g.tok + x * per_tile, bar(Q_FULL));
         }
-        ok = __shfl_sync(0xffffffffu, ok, 0);
-        ++n_seg;
-        if constexpr (!Q4) {
-          const int pages = kT >> c.log2s;  // of a tile
-          for (int t = g.t0; t < g.t1 && ok; ++t) {
-            const int live = min(pages, ((g.len - t * kT - 1) >> c.log2s) + 1);
-            int page = 0;
-            if (lane < live) page = page_of(c, g.b, t * kT + (lane << c.log2s));
-            const bool tail = g.len - t * kT < kT;
+      }
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      ++n_seg;
+      if constexpr (Q4) {
+        // a page's packed rows of one head are contiguous: a lane copies one of the tile's four parts of a page
+        const int pages = kT >> c.log2s;
+        for (int t = g.t0; t < g.t1 && ok; ++t) {
+          const int live = min(pages, ((g.len - t * kT - 1) >> c.log2s) + 1);
+          const int part = lane / 8, i = lane % 8;  // pages <= 8
+          int page = 0;
+          if (i < live) page = page_of(c, g.b, t * kT + (i << c.log2s));
+          const int slot = n_raw % kRawSlots;
+          if (n_raw >= kRawSlots)
+            ok = s2_wait(bar(RAW_EMPTY + slot), ((n_raw / kRawSlots) - 1) & 1, abort_flag, status, 1);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          if (lane == 0) mbar_arrive_expect_tx(bar(RAW_FULL + slot), (uint32_t)(live << c.log2s) * (D + 8));
+          __syncwarp();
+          if (i < live) {
+            const int bytes = part < 2 ? D / 2 : 4;  // of a row
+            const void* from = part == 0 ? c.k : part == 1 ? c.v : part == 2 ? c.k_scale : c.v_scale;
+            const uint32_t to = sb + L::kRaw + slot * L::kRawBytes + (part < 2 ? part * kT * (D / 2) : kT * D + (part - 2) * kT * 4);
+            bulk_load(to + (i << c.log2s) * bytes,
+                      static_cast<const uint8_t*>(from) + row_of(c, page, g.h, 0) * bytes,
+                      (uint32_t)bytes << c.log2s, bar(RAW_FULL + slot));
+          }
+          ++n_raw;
+        }
+      } else {
+        const int pages = kT >> c.log2s;  // of a tile
+        for (int t = g.t0; t < g.t1 && ok; ++t) {
+          const int live = min(pages, ((g.len - t * kT - 1) >> c.log2s) + 1);
+          int page = 0;
+          if (lane < live) page = page_of(c, g.b, t * kT + (lane << c.log2s));
+          const bool tail = g.len - t * kT < kT;
 #pragma unroll
-            for (int v = 0; v < 2; ++v) {
-              const int slot = e % kSlots;
-              if (e >= kSlots) ok = s2_wait(bar(KV_EMPTY + slot), ((e / kSlots) - 1) & 1, abort_flag, status, 1);
-              ok = __all_sync(0xffffffffu, ok);
-              if (!ok) break;
-              const uint32_t full = v && tail ? bar(TAIL) : bar(KV_FULL + slot);
-              if (lane == 0) mbar_arrive_expect_tx(full, (uint32_t)(live << c.log2s) * 128 * kChunks);
-              __syncwarp();
-              if (lane < live) {
-                for (int ch = 0; ch < kChunks; ++ch)
-                  tma_load_3d(sKV(slot) + ch * kChunkBytes + ((lane << c.log2s) * 128), v ? &tmV : &tmK, ch * 64, 0,
-                              page * c.heads + g.h, full);
-              }
-              if (v && tail) {
-                // rows behind the sequence may hold anything, and 0 times a NaN is a NaN
-                if (!s2_wait_drain(bar(TAIL), n_tail & 1, status, 1)) *abort_flag = 1;
-                ++n_tail;
-                const int used = g.len - t * kT;
-                for (int i = used * 8 * kChunks + lane; i < kT * 8 * kChunks; i += 32) {
-                  const int row = i / (8 * kChunks), piece = i % (8 * kChunks);
-                  st_shared_v4(sKV(slot) + (piece / 8) * kChunkBytes + row * 128 + (piece % 8) * 16, 0u, 0u, 0u, 0u);
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(KV_FULL + slot));
-              }
-              ++e;
-            }
-          }
-        }
-      } else if (warp == 9) {
-        // -------------------------------------------------------- MMA
-        if (lane == 0 && keys) {
-          constexpr uint32_t idesc_qk = umma_idesc_bf16(128, 128, 0, 0);
-          constexpr uint32_t idesc_pv = umma_idesc_bf16(128, D, 0, 1);
-#define ISSUE_QK(x, slot)                                                                              \
-  do {                                                                                                 \
-    const uint64_t a0_ = umma_desc_sw128(sQ(x), 16, 1024), b0_ = umma_desc_sw128(sKV(slot), 16, 1024); \
-    _Pragma("unroll") for (int kk = 0; kk < D / 16; ++kk) {                                            \
-      const uint64_t off_ = ((kk / 4) * kChunkBytes + (kk % 4) * 32) >> 4;                             \
-      umma_ss(tmem + (x) * 128, a0_ + off_, b0_ + off_, idesc_qk, kk > 0);                             \
-    }                                                                                                  \
-  } while (0)
-#define ISSUE_PV(x, slot, acc)                                                                  \
-  do {                                                                                          \
-    const uint64_t b0_ = umma_desc_sw128(sKV(slot), kChunkBytes, 1024);                         \
-    _Pragma("unroll") for (int kk = 0; kk < kT / 16; ++kk) {                                    \
-      umma_ts(tmem + 256 + (x) * D, tmem + (x) * 128 + 8 * kk, b0_ + (uint64_t)(kk * 2048 >> 4), \
-              idesc_pv, ((acc) || kk > 0) ? 1u : 0u);                                           \
-    }                                                                                           \
-  } while (0)
-#define WAIT_KV(i) s2_wait(bar(KV_FULL + (i) % kSlots), ((i) / kSlots) & 1, abort_flag, status, 2)
-          ok = s2_wait(bar(Q_FULL), n_seg & 1, abort_flag, status, 2);
-          ++n_seg;
-          int eK = e++;
-          if (ok) ok = WAIT_KV(eK);
-          if (ok) {
-            if (hasA) {
-              ISSUE_QK(0, eK % kSlots);
-              umma_commit(bar(S_FULL + 0));
-            }
-            if (hasB) {
-              ISSUE_QK(1, eK % kSlots);
-              umma_commit(bar(S_FULL + 1));
-            }
-            umma_commit(bar(KV_EMPTY + eK % kSlots));
-            if (g.t1 - g.t0 == 1) umma_commit(bar(Q_EMPTY));
-          }
-          for (int t = g.t0; t < g.t1 && ok; ++t) {
-            const bool more = t + 1 < g.t1;
-            const int eV = e++;
-            eK = more ? e++ : 0;
-            ok = WAIT_KV(eV);
-            if (ok && more) ok = WAIT_KV(eK);
+          for (int v = 0; v < 2; ++v) {
+            const int slot = e % kSlots;
+            if (e >= kSlots) ok = s2_wait(bar(KV_EMPTY + slot), ((e / kSlots) - 1) & 1, abort_flag, status, 1);
+            ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
-            const int sV = eV % kSlots, sK = eK % kSlots;
-            if (t <= lastA) {
-              ok = s2_wait(bar(P_FULL + 0), nA & 1, abort_flag, status, 2);
-              if (!ok) break;
-              tc_fence_after();
-              ISSUE_PV(0, sV, t > g.t0);
-              ++nA;
+            const uint32_t full = v && tail ? bar(TAIL) : bar(KV_FULL + slot);
+            if (lane == 0) mbar_arrive_expect_tx(full, (uint32_t)(live << c.log2s) * 128 * kChunks);
+            __syncwarp();
+            if (lane < live) {
+              for (int ch = 0; ch < kChunks; ++ch)
+                tma_load_3d(sKV(slot) + ch * kChunkBytes + ((lane << c.log2s) * 128), v ? &tmV : &tmK, ch * 64, 0,
+                            page * c.heads + g.h, full);
             }
-            if (more && t + 1 <= lastA) {
-              ISSUE_QK(0, sK);
-              umma_commit(bar(S_FULL + 0));
-            }
-            if (t <= lastB) {
-              ok = s2_wait(bar(P_FULL + 1), nB & 1, abort_flag, status, 2);
-              if (!ok) break;
-              tc_fence_after();
-              ISSUE_PV(1, sV, t > g.t0);
-              ++nB;
-            }
-            if (more && t + 1 <= lastB) {
-              ISSUE_QK(1, sK);
-              umma_commit(bar(S_FULL + 1));
-            }
-            umma_commit(bar(KV_EMPTY + sV));
-            if (more) {
-              umma_commit(bar(KV_EMPTY + sK));
-              if (t + 2 == g.t1) umma_commit(bar(Q_EMPTY));
-            }
-          }
-          if (ok && hasA) umma_commit(bar(O_FULL + 0));
-          if (ok && hasB) umma_commit(bar(O_FULL + 1));
-        }
-        ok = __shfl_sync(0xffffffffu, ok, 0);
-      } else if (Q4 && warp >= 10) {
-        // -------------------------------------------------------- unpacking of 4-bit pages
-        // A thread takes rows `row` and `row + 64` of each tile; the next tile's codes are on
-        // their way while this one's are unpacked.
-        if (!keys) continue;
-        const int row = threadIdx.x - 320;
-        constexpr int kWords = D / 8;  // of a row's codes
-        uint32_t wa[kWords], wb[kWords];  // rows `row`, `row + 64`: one is unpacked, one is on its way
-        size_t at[2];
-        bool use[2];
-        auto place = [&](int t) {
-#pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            const int p = t * kT + row + 64 * y;
-            use[y] = p < g.len;
-            at[y] = use[y] ? row_of(c, page_of(c, g.b, p), g.h, p) : 0;
-          }
-        };
-        auto fetch = [&](const void* codes, int y, uint32_t (&w)[kWords]) {
-          const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(codes) + at[y] * (D / 2));
-#pragma unroll
-          for (int i = 0; i < kWords / 4; ++i) {
-            uint4 x = make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);  // codes 8: zeros
-            if (use[y]) x = __ldg(src + i);
-            w[4 * i] = x.x, w[4 * i + 1] = x.y, w[4 * i + 2] = x.z, w[4 * i + 3] = x.w;
-          }
-        };
-        auto store = [&](const uint32_t (&w)[kWords], int y, int slot) {
-          // a word's 4 bytes are channels 4i .. 4i + 3 (low halves) and D/2 + 4i .. (high halves)
-#pragma unroll
-          for (int i = 0; i < kWords; i += 2)
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              uint32_t o[4];
-#pragma unroll
-              for (int z = 0; z < 2; ++z) {
-                const uint32_t x = (w[i + z] >> (4 * half)) & 0x0f0f0f0fu;
-                o[2 * z] = less_136(__byte_perm(x, 0x43u, 0x4140));
-                o[2 * z + 1] = less_136(__byte_perm(x, 0x43u, 0x4342));
+            if (v && tail) {
+              // rows behind the sequence may hold anything, and 0 times a NaN is a NaN
+              if (!s2_wait_drain(bar(TAIL), n_tail & 1, status, 1)) *abort_flag = 1;
+              ++n_tail;
+              const int used = g.len - t * kT;
+              for (int i = used * 8 * kChunks + lane; i < kT * 8 * kChunks; i += 32) {
+                const int row = i / (8 * kChunks), piece = i % (8 * kChunks);
+                st_shared_v4(sKV(slot) + (piece / 8) * kChunkBytes + row * 128 + (piece % 8) * 16, 0u, 0u, 0u, 0u);
               }
-              const int ch = half * (D / 2) + 4 * i, piece = (ch % 64) / 8;
-              st_shared_v4(sKV(slot) + (ch / 64) * kChunkBytes + (row + 64 * y) * 128 + ((piece ^ (row & 7)) << 4),
-                           o[0], o[1], o[2], o[3]);
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(bar(KV_FULL + slot));
             }
-        };
-        auto claim = [&]() -> int {  // the next tile's slot, once its products are done
-          const int slot = e % kSlots;
-          if (e >= kSlots) ok = s2_wait(bar(KV_EMPTY + slot), ((e / kSlots) - 1) & 1, abort_flag, status, 8);
-          ++e;
-          return slot;
-        };
-        place(g.t0);
-        fetch(c.k, 0, wa);
-        for (int t = g.t0; t < g.t1; ++t) {
-          fetch(c.k, 1, wb);
-          const int sK = claim();
-          if (!ok) break;
-          store(wa, 0, sK);
-          fetch(c.v, 0, wa);
-          store(wb, 1, sK);
-          fence_proxy_async_smem();
-          mbar_arrive(bar(KV_FULL + sK));
-          fetch(c.v, 1, wb);
-          const int sc = n_sc % kScaleSlots;
-          if (n_sc >= kScaleSlots)
-            ok = s2_wait(bar(SC_EMPTY + sc), ((n_sc / kScaleSlots) - 1) & 1, abort_flag, status, 8);
-          if (!ok) break;
-#pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            const float2 k2 = q4_pair(use[y] ? __ldg(static_cast<const uint32_t*>(c.k_scale) + at[y]) : 0u);
-            const float2 v2 = q4_pair(use[y] ? __ldg(static_cast<const uint32_t*>(c.v_scale) + at[y]) : 0u);
-            float2* to = reinterpret_cast<float2*>(smem + L::kScale) + sc * 2 * kT + row + 64 * y;
-            to[0] = make_float2(k2.x, fmaf(8.f, k2.x, k2.y));
-            to[kT] = make_float2(v2.x, fmaf(8.f, v2.x, v2.y));
+            ++e;
           }
-          mbar_arrive(bar(SC_FULL + sc));
-          ++n_sc;
-          const int sV = claim();
-          if (!ok) break;
-          store(wa, 0, sV);
-          if (t + 1 < g.t1) {
-            place(t + 1);
-            fetch(c.k, 0, wa);
-          }
-          store(wb, 1, sV);
-          fence_proxy_async_smem();
-          mbar_arrive(bar(KV_FULL + sV));
         }
-      } else if (warp < 8) {
-        // -------------------------------------------------------- softmax
-        const int x = warp / 4, wq = warp % 4;
-        const int r = wq * 32 + lane;  // row of the tile == TMEM lane
-        const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
-        const uint32_t tS = tmem + lane_off + x * 128;
-        const uint32_t tO = tmem + lane_off + 256 + x * D;
-        const bool has = x ? hasB : hasA;
-        const int last = x ? lastB : lastA, cnt = x ? cntB : cntA;
-        int& nS = x ? nB : nA;
-        int& nO = x ? oB : oA;
-        const int tok = r / in.g;  // of the tile
-        const bool live = tok < cnt;
-        // rows of no token see all of their tile; they are not stored
-        const int place = g.place + x * per_tile + (live ? tok : max(cnt, 1) - 1);
-        float m_used = -INFINITY, l = 0.f;
-        float vsum = 0.f, qsum = 0.f;
-        if (Q4 && keys) {
-          ok = s2_wait(bar(Q_FULL), n_seg & 1, abort_flag, status, 4);
-          ++n_seg;
-          if (ok && has && live) {
-            for (int i = 0; i < 8 * kChunks; ++i) {
-              const uint32_t at = sQ(x) + (i / 8) * kChunkBytes + r * 128 + (((i % 8) ^ (r & 7)) << 4);
-              uint32_t w[4];
-              asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                           : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                           : "r"(at));
-#pragma unroll
-              for (int z = 0; z < 4; ++z)
-                qsum += __uint_as_float(w[z] << 16) + __uint_as_float(w[z] & 0xffff0000u);
-            }
+      }
+    }
+    // copies in flight land before shared memory is released (also after an abort)
+    if (lane == 0) {
+      if constexpr (Q4) {
+        for (int d = (n_raw > kRawSlots ? n_raw - kRawSlots : 0); d < n_raw; ++d)
+          s2_wait_drain(bar(RAW_FULL + d % kRawSlots), (d / kRawSlots) & 1, status, 1);
+      } else {
+        for (int d = (e > kSlots ? e - kSlots : 0); d < e; ++d)
+          s2_wait_drain(bar(KV_FULL + d % kSlots), (d / kSlots) & 1, status, 1);
+      }
+      if (n_seg > 0) s2_wait_drain(bar(Q_FULL), (n_seg - 1) & 1, status, 1);
+    }
+    __syncwarp();
+  } else if (warp == 9) {
+    // ------------------------------------------------------------ MMA
+    int e = 0, n_seg = 0;
+    int nA = 0, nB = 0;  // key tiles of each query tile
+    FOR_SEGMENTS {
+      const Seg g = segs[si];
+      SEGMENT_OF(g)
+      if (lane == 0 && keys) {
+        constexpr uint32_t idesc_qk = umma_idesc_bf16(128, 128, 0, 0);
+        constexpr uint32_t idesc_pv = umma_idesc_bf16(128, D, 0, 1);
+#define ISSUE_QK(x, slot)                                                                              \
+do {                                                                                                 \
+  const uint64_t a0_ = umma_desc_sw128(sQ(x), 16, 1024), b0_ = umma_desc_sw128(sKV(slot), 16, 1024); \
+  _Pragma("unroll") for (int kk = 0; kk < D / 16; ++kk) {                                            \
+    const uint64_t off_ = ((kk / 4) * kChunkBytes + (kk % 4) * 32) >> 4;                             \
+    umma_ss(tmem + (x) * 128, a0_ + off_, b0_ + off_, idesc_qk, kk > 0);                             \
+  }                                                                                                  \
+} while (0)
+#define ISSUE_PV(x, slot, acc)                                                                  \
+do {                                                                                          \
+  const uint64_t b0_ = umma_desc_sw128(sKV(slot), kChunkBytes, 1024);                         \
+  _Pragma("unroll") for (int kk = 0; kk < kT / 16; ++kk) {                                    \
+    umma_ts(tmem + 256 + (x) * D, tmem + (x) * 128 + 8 * kk, b0_ + (uint64_t)(kk * 2048 >> 4), \
+            idesc_pv, ((acc) || kk > 0) ? 1u : 0u);                                           \
+  }                                                                                           \
+} while (0)
+#define WAIT_KV(i) s2_wait(bar(KV_FULL + (i) % kSlots), ((i) / kSlots) & 1, abort_flag, status, 2)
+        ok = s2_wait(bar(Q_FULL), n_seg & 1, abort_flag, status, 2);
+        ++n_seg;
+        int eK = e++;
+        if (ok) ok = WAIT_KV(eK);
+        if (ok) {
+          if (hasA) {
+            ISSUE_QK(0, eK % kSlots);
+            umma_commit(bar(S_FULL + 0));
           }
-          mbar_arrive(bar(Q_EMPTY));
+          if (hasB) {
+            ISSUE_QK(1, eK % kSlots);
+            umma_commit(bar(S_FULL + 1));
+          }
+          umma_commit(bar(KV_EMPTY + eK % kSlots));
+          if (g.t1 - g.t0 == 1) umma_commit(bar(Q_EMPTY));
         }
         for (int t = g.t0; t < g.t1 && ok; ++t) {
-          const int sc = n_sc % kScaleSlots;
-          if (t > last) {
-            if constexpr (Q4) {
-              // the other tile's keys: only counted
-              ok = s2_wait(bar(SC_FULL + sc), (n_sc / kScaleSlots) & 1, abort_flag, status, 4);
-              if (ok) mbar_arrive(bar(SC_EMPTY + sc));
-              ++n_sc;
-              continue;
-            } else {
-              break;
-            }
-          }
-          ok = s2_wait(bar(S_FULL + x), nS & 1, abort_flag, status, 4);
-          if constexpr (Q4) {
-            if (ok) ok = s2_wait(bar(SC_FULL + sc), (n_sc / kScaleSlots) & 1, abort_flag, status, 4);
-          }
+          const bool more = t + 1 < g.t1;
+          const int eV = e++;
+          eK = more ? e++ : 0;
+          ok = WAIT_KV(eV);
+          if (ok && more) ok = WAIT_KV(eK);
           if (!ok) break;
-          tc_fence_after();
-          ++nS;
-          uint32_t s[kT];
-          if constexpr (Q4) {
-            tmem_ld64(tS, *reinterpret_cast<uint32_t(*)[64]>(&s[0]));
-            tmem_ld64(tS + 64, *reinterpret_cast<uint32_t(*)[64]>(&s[64]));
-          } else {
-            tmem_ld128(tS, s);
+          const int sV = eV % kSlots, sK = eK % kSlots;
+          if (t <= lastA) {
+            ok = s2_wait(bar(P_FULL + 0), nA & 1, abort_flag, status, 2);
+            if (!ok) break;
+            tc_fence_after();
+            ISSUE_PV(0, sV, t > g.t0);
+            ++nA;
           }
-          tmem_wait_ld();
-          const uint32_t scales = sb + L::kScale + sc * 2 * kT * 8;  // {scale, min + 8 scale} of the keys, the values
-          if constexpr (Q4) {
-            const float2 q2 = make_float2(qsum, qsum);
+          if (more && t + 1 <= lastA) {
+            ISSUE_QK(0, sK);
+            umma_commit(bar(S_FULL + 0));
+          }
+          if (t <= lastB) {
+            ok = s2_wait(bar(P_FULL + 1), nB & 1, abort_flag, status, 2);
+            if (!ok) break;
+            tc_fence_after();
+            ISSUE_PV(1, sV, t > g.t0);
+            ++nB;
+          }
+          if (more && t + 1 <= lastB) {
+            ISSUE_QK(1, sK);
+            umma_commit(bar(S_FULL + 1));
+          }
+          umma_commit(bar(KV_EMPTY + sV));
+          if (more) {
+            umma_commit(bar(KV_EMPTY + sK));
+            if (t + 2 == g.t1) umma_commit(bar(Q_EMPTY));
+          }
+        }
+        if (ok && hasA) umma_commit(bar(O_FULL + 0));
+        if (ok && hasB) umma_commit(bar(O_FULL + 1));
+      }
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+    }
+    // every product is complete before tensor memory is released (also after an abort)
+    if (lane == 0) {
+      umma_commit(bar(MMA_DONE));
+      s2_wait_drain(bar(MMA_DONE), 0, status, 2);
+    }
+    __syncwarp();
+  } else if (Q4 && warp >= 10) {
+    // ------------------------------------------------------------ unpacking of 4-bit pages
+    int e = 0;
+    int n_raw = 0, n_sc = 0;  // key tiles (raw slots, scale slots)
+    FOR_SEGMENTS {
+      const Seg g = segs[si];
+      const bool keys = g.t1 > g.t0;
+      // 16 bytes of a row at a time: channels [16i, 16i + 16) in the low halves, D/2 further in the high
+      // ones.  A quarter of a warp reads 128 bytes in a row and writes 8 different banks' worth of pieces.
+      if (!keys) continue;
+      const int tid = threadIdx.x - 320;
+      constexpr int kParts = D / 32;  // of a row
+      auto unpack = [&](uint32_t raw, int slot, int used, bool centred) {
+#pragma unroll 2
+        for (int it = 0; it < 2 * kParts; ++it) {
+          const int item = it * 64 + tid, row = item / kParts, i = item % kParts;
+          uint32_t w[4];
+          asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                       : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                       : "r"(raw + item * 16));
+          // rows behind the sequence: zeros as values (their weight is 0 and 0 times anything must be 0)
+          if (row >= used) w[0] = w[1] = w[2] = w[3] = 0x88888888u;
 #pragma unroll
-            for (int col = 0; col < kT; col += 2) {
-              const float4 a = ld_shared_f4(scales + col * 8);
-              const float2 v = __ffma2_rn(make_float2(__uint_as_float(s[col]), __uint_as_float(s[col + 1])),
-                                          make_float2(a.x, a.z), __fmul2_rn(make_float2(a.y, a.w), q2));
-              s[col] = __float_as_uint(v.x);
-              s[col + 1] = __float_as_uint(v.y);
+          for (int half = 0; half < 2; ++half) {
+            uint32_t o[8];
+#pragma unroll
+            for (int z = 0; z < 4; ++z) {
+              const uint32_t x = (w[z] >> (4 * half)) & 0x0f0f0f0fu;
+              o[2 * z] = __byte_perm(x, 0x43u, 0x4140);  // 0x43, code: 128 + code in bf16
+              o[2 * z + 1] = __byte_perm(x, 0x43u, 0x4342);
             }
+            if (centred) {
+#pragma unroll
+              for (int z = 0; z < 8; ++z) o[z] = less_136(o[z]);
+            }
+            const int ch = half * (D / 2) + 16 * i, piece = (ch % 64) / 8;
+            const uint32_t to = sKV(slot) + (ch / 64) * kChunkBytes + row * 128;
+            st_shared_v4(to + ((piece ^ (row & 7)) << 4), o[0], o[1], o[2], o[3]);
+            st_shared_v4(to + (((piece + 1) ^ (row & 7)) << 4), o[4], o[5], o[6], o[7]);
           }
-          const int cmax = min(kT, max(0, place + 1 - t * kT));
-          if (!__all_sync(0xffffffffu, cmax == kT)) {
+        }
+      };
+      auto claim = [&]() -> int {  // the next tile's slot, once its products are done
+        const int slot = e % kSlots;
+        if (e >= kSlots) ok = s2_wait(bar(KV_EMPTY + slot), ((e / kSlots) - 1) & 1, abort_flag, status, 8);
+        ++e;
+        return slot;
+      };
+      for (int t = g.t0; t < g.t1; ++t) {
+        const int rs = n_raw % kRawSlots, sc = n_sc % kScaleSlots, used = g.len - t * kT;
+        const uint32_t raw = sb + L::kRaw + rs * L::kRawBytes;
+        ok = s2_wait(bar(RAW_FULL + rs), (n_raw / kRawSlots) & 1, abort_flag, status, 8);
+        if (!ok) break;
+        const int sK = claim();
+        if (!ok) break;
+        unpack(raw, sK, kT, false);  // rows behind the sequence are masked as keys
+        fence_proxy_async_smem();
+        mbar_arrive(bar(KV_FULL + sK));
+        if (n_sc >= kScaleSlots)
+          ok = s2_wait(bar(SC_EMPTY + sc), ((n_sc / kScaleSlots) - 1) & 1, abort_flag, status, 8);
+        if (!ok) break;
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          const int row = tid + 64 * y;
+          const uint32_t* pairs = reinterpret_cast<const uint32_t*>(smem + L::kRaw + rs * L::kRawBytes + kT * D);
+          const float2 k2 = q4_pair(row < used ? pairs[row] : 0u), v2 = q4_pair(row < used ? pairs[kT + row] : 0u);
+          float2* to = reinterpret_cast<float2*>(smem + L::kScale) + sc * 2 * kT + row;
+          to[0] = make_float2(k2.x, fmaf(-128.f, k2.x, k2.y));  // codes come as 128 + code,
+          to[kT] = make_float2(v2.x, fmaf(8.f, v2.x, v2.y));    // and as code - 8
+        }
+        mbar_arrive(bar(SC_FULL + sc));
+        ++n_sc;
+        const int sV = claim();
+        if (!ok) break;
+        unpack(raw + kT * (D / 2), sV, used, true);
+        fence_proxy_async_smem();
+        mbar_arrive(bar(KV_FULL + sV));
+        mbar_arrive(bar(RAW_EMPTY + rs));
+        ++n_raw;
+      }
+    }
+  } else if (warp < 8) {
+    // ------------------------------------------------------------ softmax
+    const int x = warp / 4, wq = warp % 4;
+    const int r = wq * 32 + lane;  // row of the tile == TMEM lane
+    const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
+    const uint32_t tS = tmem + lane_off + x * 128;
+    const uint32_t tO = tmem + lane_off + 256 + x * D;
+    const int tok = r / in.g;  // of the tile
+    int nS = 0, nO = 0;        // key tiles, and segments with keys, of this query tile
+    int n_seg = 0, n_sc = 0;
+    FOR_SEGMENTS {
+      const Seg& g = segs[si];
+      const bool keys = g.t1 > g.t0;
+      const int cnt = x ? min(g.left - per_tile, per_tile) : min(g.left, per_tile);
+      const int last = min(last_tile(g.place + x * per_tile, cnt), g.t1 - 1);
+      const bool has = last >= g.t0;
+      const bool live = tok < cnt;
+      // rows of no token see all of their tile; they are not stored
+      const int place = g.place + x * per_tile + (live ? tok : max(cnt, 1) - 1);
+      float m_used = -INFINITY, l = 0.f;
+      float vsum = 0.f, qsum = 0.f;
+      if (Q4 && keys) {
+        ok = s2_wait(bar(Q_FULL), n_seg & 1, abort_flag, status, 4);
+        ++n_seg;
+        if (ok && has && live) {
+          for (int i = 0; i < 8 * kChunks; ++i) {
+            const uint32_t at = sQ(x) + (i / 8) * kChunkBytes + r * 128 + (((i % 8) ^ (r & 7)) << 4);
+            uint32_t w[4];
+            asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                         : "r"(at));
+#pragma unroll
+            for (int z = 0; z < 4; ++z)
+              qsum += __uint_as_float(w[z] << 16) + __uint_as_float(w[z] & 0xffff0000u);
+          }
+        }
+        mbar_arrive(bar(Q_EMPTY));
+      }
+      for (int t = g.t0; t < g.t1 && ok; ++t) {
+        const int sc = n_sc % kScaleSlots;
+        if (t > last) {
+          if constexpr (Q4) {
+            // the other tile's keys: only counted
+            ok = s2_wait(bar(SC_FULL + sc), (n_sc / kScaleSlots) & 1, abort_flag, status, 4);
+            if (ok) mbar_arrive(bar(SC_EMPTY + sc));
+            ++n_sc;
+            continue;
+          } else {
+            break;
+          }
+        }
+        ok = s2_wait(bar(S_FULL + x), nS & 1, abort_flag, status, 4);
+        if constexpr (Q4) {
+          if (ok) ok = s2_wait(bar(SC_FULL + sc), (n_sc / kScaleSlots) & 1, abort_flag, status, 4);
+        }
+        if (!ok) break;
+        tc_fence_after();
+        ++nS;
+        const int cmax = min(kT, max(0, place + 1 - t * kT));
+        const bool cut = !__all_sync(0xffffffffu, cmax == kT);
+        float factor = 1.f;  // by which the maximum's growth shrinks what was summed before
+        bool need = false;
+        uint32_t s[Q4 ? 64 : kT];   // scores
+        const float2 c2 = make_float2(in.scale_log2, in.scale_log2);
+        if constexpr (Q4) {
+          // Half a tile at a time: 64 scores, their keys' pairs, 32 words of weights.
+          const uint32_t scales = sb + L::kScale + sc * 2 * kT * 8;
+          const float2 q2 = make_float2(qsum, qsum);
+#pragma unroll 1
+          for (int half = 0; half < 2; ++half) {
+            Pairs8 pr[2];
+            load_pairs(pr[0], scales + half * 64 * 8);
+            tmem_ld64(tS + 64 * half, *reinterpret_cast<uint32_t(*)[64]>(&s[0]));
+            tmem_wait_ld();
+#pragma unroll
+            for (int col = 0; col < 64; col += 8) {
+              if (col + 8 < 64) load_pairs(pr[(col / 8 + 1) & 1], scales + (half * 64 + col + 8) * 8);
+#pragma unroll
+              for (int z = 0; z < 4; ++z) {
+                const float4 a = pr[(col / 8) & 1].p[z];  // {scale, min} of two keys
+                const int i = col + 2 * z;
+                const float2 v = __ffma2_rn(make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])),
+                                            make_float2(a.x, a.z), __fmul2_rn(make_float2(a.y, a.w), q2));
+                s[i] = __float_as_uint(v.x);
+                s[i + 1] = __float_as_uint(v.y);
+              }
+            }
+            if (cut) {
+#pragma unroll
+              for (int col = 0; col < 64; ++col)
+                if (64 * half + col >= cmax) s[col] = 0xff800000u;  // -inf
+            }
+            float mq[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+            for (int col = 0; col < 64; col += 4) {
+              mq[0] = fmax3(mq[0], __uint_as_float(s[col]), __uint_as_float(s[col + 1]));
+              mq[1] = fmax3(mq[1], __uint_as_float(s[col + 2]), __uint_as_float(s[col + 3]));
+            }
+            const float m_new = fmaxf(m_used, fmaxf(mq[0], mq[1]) * in.scale_log2);
+            const bool grow = m_new > m_used + 8.0f;
+            float f = 1.f;
+            if (grow) {
+              f = ex2(m_used - m_new);
+              l *= f;
+              vsum *= f;
+              factor *= f;
+              need = true;
+              m_used = m_new;
+            }
+            if (half == 1 && __any_sync(0xffffffffu, grow)) {  // the first half's weights have been written already
+              uint32_t w[32];
+              tmem_wait_st();
+              tmem_ld32(tS, w);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                w[i] = pack_bf16(__uint_as_float(w[i] << 16) * f, __uint_as_float(w[i] & 0xffff0000u) * f);
+              tmem_st32(tS, w);
+            }
+            const float m_exp = (m_used == -INFINITY) ? 0.f : m_used;
+            const float2 nm2 = make_float2(-m_exp, -m_exp);
+            float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)}, vacc = make_float2(0.f, 0.f);
+            uint32_t pk[32];
+            load_pairs(pr[0], scales + (kT + half * 64) * 8);
+#pragma unroll
+            for (int col = 0; col < 64; col += 8) {
+              if (col + 8 < 64) load_pairs(pr[(col / 8 + 1) & 1], scales + (kT + half * 64 + col + 8) * 8);
+#pragma unroll
+              for (int z = 0; z < 4; ++z) {
+                const float4 u = pr[(col / 8) & 1].p[z];
+                const int i = col + 2 * z;
+                const float2 a =
+                    __ffma2_rn(make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), c2, nm2);
+                const float2 w = make_float2(ex2(a.x), ex2(a.y));
+                acc[z & 1] = __fadd2_rn(acc[z & 1], w);
+                vacc = __ffma2_rn(w, make_float2(u.y, u.w), vacc);
+                const float2 ws = __fmul2_rn(w, make_float2(u.x, u.z));
+                pk[i / 2] = pack_bf16(ws.x, ws.y);
+              }
+            }
+            const float2 sum = __fadd2_rn(acc[0], acc[1]);
+            l += sum.x + sum.y;
+            vsum += vacc.x + vacc.y;
+            tmem_st32(tS + 32 * half, pk);
+          }
+          mbar_arrive(bar(SC_EMPTY + sc));
+          ++n_sc;
+        } else {
+          tmem_ld128(tS, *reinterpret_cast<uint32_t(*)[kT]>(&s[0]));
+          tmem_wait_ld();
+          if (cut) {
 #pragma unroll
             for (int col = 0; col < kT; ++col)
               if (col >= cmax) s[col] = 0xff800000u;  // -inf
@@ -612,126 +751,97 @@ __global__ void __launch_bounds__(chunk::threads<Q4>(), 1)
           }
           const float mx = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3])) * in.scale_log2;
           const float m_new = fmaxf(m_used, mx);
-          const bool need = m_new > m_used + 8.0f;
-          float factor = 1.f;
+          need = m_new > m_used + 8.0f;
           if (need) {
             factor = ex2(m_used - m_new);
             l *= factor;
-            vsum *= factor;
             m_used = m_new;
           }
           const float m_exp = (m_used == -INFINITY) ? 0.f : m_used;
-          const float2 c2 = make_float2(in.scale_log2, in.scale_log2);
           const float2 nm2 = make_float2(-m_exp, -m_exp);
           float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-          float2 vacc = make_float2(0.f, 0.f);
 #pragma unroll
           for (int col = 0; col < kT; col += 2) {
             const float2 a =
                 __ffma2_rn(make_float2(__uint_as_float(s[col]), __uint_as_float(s[col + 1])), c2, nm2);
-            float2 p = make_float2(ex2(a.x), ex2(a.y));
-            acc[(col / 2) & 3] = __fadd2_rn(acc[(col / 2) & 3], p);
-            if constexpr (Q4) {
-              const float4 u = ld_shared_f4(scales + (kT + col) * 8);
-              vacc = __ffma2_rn(p, make_float2(u.y, u.w), vacc);
-              p = __fmul2_rn(p, make_float2(u.x, u.z));
-            }
-            s[col / 2] = pack_bf16(p.x, p.y);
+            const float2 w = make_float2(ex2(a.x), ex2(a.y));
+            acc[(col / 2) & 3] = __fadd2_rn(acc[(col / 2) & 3], w);
+            s[col / 2] = pack_bf16(w.x, w.y);
           }
           const float2 sum = __fadd2_rn(__fadd2_rn(acc[0], acc[1]), __fadd2_rn(acc[2], acc[3]));
           l += sum.x + sum.y;
-          vsum += vacc.x + vacc.y;
-          if constexpr (Q4) {
-            mbar_arrive(bar(SC_EMPTY + sc));
-            ++n_sc;
-          }
-          // S(t) was issued behind O += P V of tile t - 1, so O is complete here
-          if (t > g.t0 && __any_sync(0xffffffffu, need)) {
-            const float f = need ? factor : 1.f;
-#pragma unroll
-            for (int j = 0; j < D / 32; ++j) {
-              uint32_t o[32];
-              tmem_ld32(tO + j * 32, o);
-              tmem_wait_ld();
-#pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-              tmem_st32(tO + j * 32, o);
-            }
-            tmem_wait_st();
-          }
-          tmem_st64(tS, *reinterpret_cast<const uint32_t(*)[64]>(&s[0]));
-          tmem_wait_st();
-          tc_fence_before();
-          mbar_arrive(bar(P_FULL + x));
         }
-        if (ok && has) {
-          ok = s2_wait(bar(O_FULL + x), nO & 1, abort_flag, status, 4);
-          ++nO;
-          tc_fence_after();
-        }
-        // ------------------------------------------------------ rows out
-        if (ok) {
-          const size_t out = (size_t)(g.tok + x * per_tile + tok) * in.heads + g.h * in.g + r % in.g;
-          const float inv = l > 0.f ? 1.f / l : 0.f;
-          float* part = in.partial + ((size_t)g.slot * 2 * kT + x * kT + r) * (D + 4);
+        // S(t) was issued behind O += P V of tile t - 1, so O is complete here
+        if (t > g.t0 && __any_sync(0xffffffffu, need)) {
 #pragma unroll
           for (int j = 0; j < D / 32; ++j) {
             uint32_t o[32];
-            if (has) {
-              tmem_ld32(tO + j * 32, o);
-              tmem_wait_ld();
-            } else {
+            tmem_ld32(tO + j * 32, o);
+            tmem_wait_ld();
 #pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] = 0u;
-            }
-            if (live) {
-              if (g.slot < 0) {
-                uint4* dst = reinterpret_cast<uint4*>(in.o + out * D + j * 32);
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * factor);
+            tmem_st32(tO + j * 32, o);
+          }
+          tmem_wait_st();
+        }
+        if constexpr (!Q4) tmem_st64(tS, *reinterpret_cast<const uint32_t(*)[64]>(&s[0]));
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(bar(P_FULL + x));
+      }
+      if (ok && has) {
+        ok = s2_wait(bar(O_FULL + x), nO & 1, abort_flag, status, 4);
+        ++nO;
+        tc_fence_after();
+      }
+      // ------------------------------------------------------ rows out
+      if (ok) {
+        const size_t out = (size_t)(g.tok + x * per_tile + tok) * in.heads + g.h * in.g + r % in.g;
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+        float* part = in.partial + ((size_t)g.slot * 2 * kT + x * kT + r) * (D + 4);
 #pragma unroll
-                for (int i = 0; i < 32; i += 8) {
-                  uint32_t w[4];
+        for (int j = 0; j < D / 32; ++j) {
+          uint32_t o[32];
+          if (has) {
+            tmem_ld32(tO + j * 32, o);
+            tmem_wait_ld();
+          } else {
 #pragma unroll
-                  for (int z = 0; z < 4; ++z)
-                    w[z] = pack_bf16((__uint_as_float(o[i + 2 * z]) + vsum) * inv,
-                                     (__uint_as_float(o[i + 2 * z + 1]) + vsum) * inv);
-                  dst[i / 8] = make_uint4(w[0], w[1], w[2], w[3]);
-                }
-              } else {
-                float4* dst = reinterpret_cast<float4*>(part + j * 32);
-#pragma unroll
-                for (int i = 0; i < 32; i += 4)
-                  dst[i / 4] = make_float4(__uint_as_float(o[i]) + vsum, __uint_as_float(o[i + 1]) + vsum,
-                                           __uint_as_float(o[i + 2]) + vsum, __uint_as_float(o[i + 3]) + vsum);
-              }
-            }
+            for (int i = 0; i < 32; ++i) o[i] = 0u;
           }
           if (live) {
             if (g.slot < 0) {
-              if (in.lse) in.lse[out] = l > 0.f ? (m_used + log2f(l)) * 0.69314718055994531f : -INFINITY;
+              uint4* dst = reinterpret_cast<uint4*>(in.o + out * D + j * 32);
+#pragma unroll
+              for (int i = 0; i < 32; i += 8) {
+                uint32_t w[4];
+#pragma unroll
+                for (int z = 0; z < 4; ++z)
+                  w[z] = pack_bf16((__uint_as_float(o[i + 2 * z]) + vsum) * inv,
+                                   (__uint_as_float(o[i + 2 * z + 1]) + vsum) * inv);
+                dst[i / 8] = make_uint4(w[0], w[1], w[2], w[3]);
+              }
             } else {
-              *reinterpret_cast<float4*>(part + D) = make_float4(m_used, l, 0.f, 0.f);
+              float4* dst = reinterpret_cast<float4*>(part + j * 32);
+#pragma unroll
+              for (int i = 0; i < 32; i += 4)
+                dst[i / 4] = make_float4(__uint_as_float(o[i]) + vsum, __uint_as_float(o[i + 1]) + vsum,
+                                         __uint_as_float(o[i + 2]) + vsum, __uint_as_float(o[i + 3]) + vsum);
             }
           }
-          tc_fence_before();  // O has been read: ordered before the next unit's first P_FULL arrival
         }
+        if (live) {
+          if (g.slot < 0) {
+            if (in.lse) in.lse[out] = l > 0.f ? (m_used + log2f(l)) * 0.69314718055994531f : -INFINITY;
+          } else {
+            *reinterpret_cast<float4*>(part + D) = make_float4(m_used, l, 0.f, 0.f);
+          }
+        }
+        tc_fence_before();  // O has been read: ordered before the next unit's first P_FULL arrival
       }
     }
-    __syncthreads();
   }
 
-  // Copies and products in flight land before shared and tensor memory are released (also after an abort).
-  if (warp == 8 && lane == 0) {
-    if constexpr (!Q4) {
-      for (int d = (e > kSlots ? e - kSlots : 0); d < e; ++d)
-        s2_wait_drain(bar(KV_FULL + d % kSlots), (d / kSlots) & 1, status, 1);
-    }
-    if (n_seg > 0) s2_wait_drain(bar(Q_FULL), (n_seg - 1) & 1, status, 1);
-  }
-  if (warp == 9 && lane == 0) {
-    umma_commit(bar(MMA_DONE));
-    s2_wait_drain(bar(MMA_DONE), 0, status, 2);
-  }
-  __syncwarp();
   tc_fence_before();
   __syncthreads();
   if (warp == 9) {
@@ -740,6 +850,8 @@ __global__ void __launch_bounds__(chunk::threads<Q4>(), 1)
   }
 }
 
+#undef FOR_SEGMENTS
+#undef SEGMENT_OF
 #undef ISSUE_QK
 #undef ISSUE_PV
 #undef WAIT_KV
@@ -761,12 +873,11 @@ __global__ void __launch_bounds__(256) s2_cache_chunk_join_kernel(const __grid_c
     const Seq s = load_seq(c, b);
     return s.n > 0 ? Units(s, per_tile).head() * c.heads : 0;
   };
-  const Line line = make_line<kThreads>(c.B, in.pieces, in.min_piece, sh, weight_of);
-  const long long cut = line.piece * (blockIdx.x + 1);
-  if (cut >= line.total) return;
   int b;
   long long start;
-  find_seq<kThreads>(c.B, cut, sh, weight_of, b, start);
+  const Line line = find_piece<kThreads>(c.B, in.pieces, in.min_piece, blockIdx.x + 1, sh, weight_of, b, start);
+  const long long cut = line.piece * (blockIdx.x + 1);
+  if (cut >= line.total) return;
   const Seq s = load_seq(c, b);
   const Units u(s, per_tile);
   const int h = (int)((cut - start) / u.head());

@@ -208,7 +208,7 @@ int s2attn_cache_attn(const s2_cache* cache, const s2_cache_batch* batch, const 
                     "cache attention");
   }
   in.pieces = s2::kChunkPieces;
-  in.min_piece = 512;
+  in.min_piece = 2048;  // keys: less is not worth a second launch's reading of partial sums
   const uint64_t S = (uint64_t)cache->page_size, d = (uint64_t)D, blocks = (uint64_t)(cache->pages * cache->heads);
   CUtensorMap tq, tk, tv;
   if ((rc = s2::encode_map(&tq, q, {d, (uint64_t)heads, (uint64_t)batch->tokens}, {d * 2, (uint64_t)ldq * 2},
