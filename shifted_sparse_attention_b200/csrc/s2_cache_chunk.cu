@@ -92,7 +92,7 @@ struct Layout {
   static constexpr int kKVBytes = kT * D * 2;
   static constexpr int kQ = 0;
   static constexpr int kKV = 2 * kQBytes;
-  static constexpr int kScale = kKV + slots<Q4>() * kKVBytes;  // per slot {sk, mk'} of the keys, then {sv, mv'}
+  static constexpr int kScale = kKV + slots<Q4>() * kKVBytes;  // per slot {s, s, m, m} of each two keys, then the same of the values
   // packed rows of a key tile: key codes, value codes, key pairs, value pairs
   static constexpr int kRaw = kScale + (Q4 ? kScaleSlots * kT * 16 : 0);
   static constexpr int kRawBytes = kT * (D + 8);
@@ -187,7 +187,7 @@ __device__ __noinline__ int walk_on(Walk& w, const CacheArgs& c, int per_tile, S
   return k;
 }
 
-// {scale, min} of eight keys, the same for all lanes: four loads at once, so that their wait is shared.
+// {scale, scale, min, min} of four times two keys, the same for all lanes: four loads at once, so that their wait is shared.
 // The clobber keeps them where they stand: moved up together they would fill the registers.
 struct Pairs8 {
   float4 p[4];
@@ -572,9 +572,12 @@ do {                                                                            
           const int row = tid + 64 * y;
           const uint32_t* pairs = reinterpret_cast<const uint32_t*>(smem + L::kRaw + rs * L::kRawBytes + kT * D);
           const float2 k2 = q4_pair(row < used ? pairs[row] : 0u), v2 = q4_pair(row < used ? pairs[kT + row] : 0u);
-          float2* to = reinterpret_cast<float2*>(smem + L::kScale) + sc * 2 * kT + row;
-          to[0] = make_float2(k2.x, fmaf(-128.f, k2.x, k2.y));  // codes come as 128 + code,
-          to[kT] = make_float2(v2.x, fmaf(8.f, v2.x, v2.y));    // and as code - 8
+          // {scale, scale, min, min} of two keys: adjacent registers for the softmax's packed arithmetic
+          float* to = reinterpret_cast<float*>(smem + L::kScale) + sc * 4 * kT + (row / 2) * 4 + row % 2;
+          to[0] = k2.x;
+          to[2] = fmaf(-128.f, k2.x, k2.y);  // codes come as 128 + code,
+          to[2 * kT] = v2.x;
+          to[2 * kT + 2] = fmaf(8.f, v2.x, v2.y);  // and as code - 8
         }
         mbar_arrive(bar(SC_FULL + sc));
         ++n_sc;
@@ -666,10 +669,10 @@ do {                                                                            
               if (col + 8 < 64) load_pairs(pr[(col / 8 + 1) & 1], scales + (half * 64 + col + 8) * 8);
 #pragma unroll
               for (int z = 0; z < 4; ++z) {
-                const float4 a = pr[(col / 8) & 1].p[z];  // {scale, min} of two keys
+                const float4 a = pr[(col / 8) & 1].p[z];  // {scale, scale, min, min} of two keys
                 const int i = col + 2 * z;
                 const float2 v = __ffma2_rn(make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])),
-                                            make_float2(a.x, a.z), __fmul2_rn(make_float2(a.y, a.w), q2));
+                                            make_float2(a.x, a.y), __fmul2_rn(make_float2(a.z, a.w), q2));
                 s[i] = __float_as_uint(v.x);
                 s[i + 1] = __float_as_uint(v.y);
               }
@@ -722,8 +725,8 @@ do {                                                                            
                     __ffma2_rn(make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), c2, nm2);
                 const float2 w = make_float2(ex2(a.x), ex2(a.y));
                 acc[z & 1] = __fadd2_rn(acc[z & 1], w);
-                vacc = __ffma2_rn(w, make_float2(u.y, u.w), vacc);
-                const float2 ws = __fmul2_rn(w, make_float2(u.x, u.z));
+                vacc = __ffma2_rn(w, make_float2(u.z, u.w), vacc);
+                const float2 ws = __fmul2_rn(w, make_float2(u.x, u.y));
                 pk[i / 2] = pack_bf16(ws.x, ws.y);
               }
             }
