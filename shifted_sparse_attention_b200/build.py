@@ -18,7 +18,7 @@ LIB = PKG / "libs2attn.so"
 DEBUG_LIB = PKG / "libs2attn_debug.so"
 SOURCES = ["s2attn_api.cu", "s2_fwd.cu", "s2_bwd.cu", "s2_adj.cu", "s2_docs.cu", "s2_gap.cu", "s2_rope.cu", "s2_sp.cu", "s2attn_noalloc.cu",
            "s2attn_cache.cu", "s2_cache_append.cu", "s2_cache_attn.cu", "s2_cache_chunk.cu"]
-HEADERS = ["s2_index.cuh", "sm100_ptx.cuh", "s2_kernels.h", "s2_debug.cuh", "s2_cache.cuh"]
+HEADERS = ["s2_index.cuh", "sm100_ptx.cuh", "s2_kernels.h", "s2_debug.cuh", "s2_cache.cuh", "s2_cache_join.cuh"]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",

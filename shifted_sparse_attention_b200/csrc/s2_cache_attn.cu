@@ -34,6 +34,7 @@
 #include <cuda_runtime.h>
 
 #include "s2_cache.cuh"
+#include "s2_cache_join.cuh"
 #include "s2_kernels.h"
 #include "sm100_ptx.cuh"
 
@@ -174,12 +175,6 @@ __device__ __forceinline__ long long seq_steps(const CacheArgs& c, const AttnIn&
 }
 
 }  // namespace
-
-// Partial sums of a piece's unit: per row D floats of O, then max and sum.
-template <int D>
-__host__ __device__ constexpr int partial_floats(int rows) {
-  return rows * (D + 2);
-}
 
 // 16-key blocks of a step: what a warp has in flight, against its registers.
 template <bool Q4>
@@ -527,7 +522,7 @@ __global__ void __launch_bounds__(W * 32, ctas_per_sm<NR, W>())
     __syncthreads();
     // four channels of a row a thread; rows of no token are left out
     const int rows_here = min(kRows, seq.n * in.g - rb * kRows);
-    float* part = in.partial + (size_t)(2 * blockIdx.x + (unit_first < x0 ? 0 : 1)) * partial_floats<D>(kRows);
+    float* part = in.partial + (size_t)(2 * blockIdx.x + (unit_first < x0 ? 0 : 1)) * kRows * kPartial<D>;
     for (int i = threadIdx.x; i < rows_here * (D / 4); i += kThreads) {
       const int row = i / (D / 4), d = 4 * (i % (D / 4));
       float mm = sh.m[0][row];
@@ -551,11 +546,8 @@ __global__ void __launch_bounds__(W * 32, ctas_per_sm<NR, W>())
             make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
         if (in.lse && d == 0) in.lse[out] = ll > 0.f ? (mm + log2f(ll)) * 0.69314718055994531f : -INFINITY;
       } else {
-        *reinterpret_cast<float4*>(part + row * D + d) = o;
-        if (d == 0) {
-          part[kRows * D + 2 * row] = mm;
-          part[kRows * D + 2 * row + 1] = ll;
-        }
+        *reinterpret_cast<float4*>(part + row * kPartial<D> + d) = o;
+        if (d == 0) *reinterpret_cast<float2*>(part + row * kPartial<D> + D) = make_float2(mm, ll);
       }
     }
     __syncthreads();
@@ -563,22 +555,18 @@ __global__ void __launch_bounds__(W * 32, ctas_per_sm<NR, W>())
 }
 
 // Joins the partial sums of units that the line's cuts run through.  CTA i
-// stands for cut i + 1; the CTAs of one unit's cuts share its rows and
-// channels out among them.  The order of the sum is the pieces'.
+// stands for cut i + 1; the CTAs of one unit's cuts share its rows out.
 template <int D, bool Q4, int NR, int W>
-__global__ void __launch_bounds__(128) s2_cache_join_kernel(const __grid_constant__ CacheArgs c,
-                                                            const __grid_constant__ AttnIn in) {
-  constexpr int kThreads = 128, kWarps = kThreads / 32;
+__global__ void __launch_bounds__(kJoinThreads) s2_cache_join_kernel(const __grid_constant__ CacheArgs c,
+                                                                     const __grid_constant__ AttnIn in) {
   constexpr int kStep = 16 * step_blocks<Q4>();
   constexpr int kRows = 8 * NR;
-  constexpr int kGroups = kThreads / 8;  // partial sums added side by side, 8 lanes of 4 channels each
-  __shared__ long long sh[kWarps + 2];
-  __shared__ float s_red[2][kWarps];
-  __shared__ float4 s_o[kGroups][8];
+  __shared__ JoinShared<D> sh;
   auto weight = [&](int i) { return seq_steps<NR, W>(c, in, i, kStep); };
   int b;
   long long seq_first;
-  const Line line = find_piece<kThreads>(c.B, in.pieces, in.min_piece, blockIdx.x + 1, sh, weight, b, seq_first);
+  const Line line =
+      find_piece<kJoinThreads>(c.B, in.pieces, in.min_piece, blockIdx.x + 1, sh.line, weight, b, seq_first);
   const long long cut = line.piece * (blockIdx.x + 1);
   if (cut >= line.total) return;
   const Seq seq = load_seq(c, b);
@@ -587,65 +575,18 @@ __global__ void __launch_bounds__(128) s2_cache_join_kernel(const __grid_constan
   const long long first = seq_first + unit * span + unit_steps<W>(), last = first + steps - 1;  // of its steps
   if (cut <= first) return;  // the cut lies before the unit's first step
   const int p0 = (int)(first / line.piece), p1 = (int)(last / line.piece);  // pieces that hold its steps
-  const int nth = (int)blockIdx.x - p0, helpers = p1 - p0;
   const int h = (int)(unit / blocks), rb = (int)(unit % blocks);
-  const int rows_here = min(kRows, seq.n * in.g - rb * kRows);
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  // a piece's first partial unit is one that began before it
-  auto part_of = [&](int p) -> const float* {
-    const int slot = 2 * p + (first < line.piece * p ? 0 : 1);
-    return in.partial + (size_t)slot * partial_floats<D>(kRows);
-  };
-  const int group = threadIdx.x / 8, e = threadIdx.x % 8, lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  for (int item = nth; item < rows_here * (D / 32); item += helpers) {
-    const int row = item / (D / 32), d = 32 * (item % (D / 32)) + 4 * e;
-    float mm = -INFINITY;
-    for (int p = p0 + threadIdx.x; p <= p1; p += kThreads) mm = fmaxf(mm, part_of(p)[kRows * D + 2 * row]);
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, off));
-    __syncthreads();
-    if (lane == 0) s_red[0][warp] = mm;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, s_red[0][w]);
-    float ll = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (mm != -INFINITY) {
-#pragma unroll 4
-      for (int p = p0 + group; p <= p1; p += kGroups) {
-        const float* part = part_of(p);
-        const float2 ml = *reinterpret_cast<const float2*>(part + kRows * D + 2 * row);
-        const float4 v = *reinterpret_cast<const float4*>(part + row * D + d);
-        const float f = ex2(ml.x - mm);
-        ll += ml.y * f;
-        o.x += v.x * f, o.y += v.y * f, o.z += v.z * f, o.w += v.w * f;
-      }
-    }
-    s_o[group][e] = o;
-    // every lane of a group holds the group's sum of weights; one of each group counts
-    float lw = e == 0 ? ll : 0.f;
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) lw += __shfl_xor_sync(0xffffffffu, lw, off);
-    if (lane == 0) s_red[1][warp] = lw;
-    __syncthreads();
-    if (threadIdx.x < 8) {
-      float4 t = s_o[0][threadIdx.x];
-#pragma unroll
-      for (int i = 1; i < kGroups; ++i) {
-        const float4 v = s_o[i][threadIdx.x];
-        t.x += v.x, t.y += v.y, t.z += v.z, t.w += v.w;
-      }
-      float lt = 0.f;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) lt += s_red[1][w];
-      const int at = rb * kRows + row;
-      const size_t out = (size_t)(seq.first + at / in.g) * in.heads + h * in.g + at % in.g;
-      const float inv = lt > 0.f ? 1.f / lt : 0.f;
-      *reinterpret_cast<uint2*>(in.o + out * D + d) =
-          make_uint2(pack_bf16(t.x * inv, t.y * inv), pack_bf16(t.z * inv, t.w * inv));
-      if (in.lse && d == 0) in.lse[out] = lt > 0.f ? (mm + log2f(lt)) * 0.69314718055994531f : -INFINITY;
-    }
-  }
+  join_rows<D>(
+      sh, min(kRows, seq.n * in.g - rb * kRows), (int)blockIdx.x - p0, p1 - p0, p0, p1,
+      [&](int p, int row) {  // a piece's first partial unit is one that began before it
+        return in.partial + ((size_t)(2 * p + (first < line.piece * p ? 0 : 1)) * kRows + row) * kPartial<D>;
+      },
+      [&](int row) {
+        const int at = rb * kRows + row;
+        return (size_t)(seq.first + at / in.g) * in.heads + h * in.g + at % in.g;
+      },
+      in.o, in.lse);
 }
 
 template <int D, bool Q4, int NR, int W>
@@ -664,7 +605,7 @@ static int decode_impl(const CacheArgs& c, const AttnIn& in0, cudaStream_t strea
   if (e != cudaSuccess) return (int)e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(in.pieces - 1);
-  cfg.blockDim = dim3(128);
+  cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = stream;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -684,6 +625,6 @@ int launch_cache_decode(const CacheArgs& c, const AttnIn& in, int D, bool q4, in
   return q4 ? decode_rows<128, true>(c, in, rows, stream) : decode_rows<128, false>(c, in, rows, stream);
 }
 
-size_t cache_decode_partial_bytes(int D) { return (size_t)2 * kDecodePieces * 16 * (D + 2) * sizeof(float); }
+size_t cache_decode_partial_bytes(int D) { return (size_t)2 * kDecodePieces * 16 * (D + 4) * sizeof(float); }
 
 }  // namespace s2

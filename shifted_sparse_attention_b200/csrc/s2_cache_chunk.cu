@@ -32,6 +32,7 @@
 #include <cuda_runtime.h>
 
 #include "s2_cache.cuh"
+#include "s2_cache_join.cuh"
 #include "s2_kernels.h"
 #include "sm100_ptx.cuh"
 
@@ -801,7 +802,7 @@ do {                                                                            
       if (ok) {
         const size_t out = (size_t)(g.tok + x * per_tile + tok) * in.heads + g.h * in.g + r % in.g;
         const float inv = l > 0.f ? 1.f / l : 0.f;
-        float* part = in.partial + ((size_t)g.slot * 2 * kT + x * kT + r) * (D + 4);
+        float* part = in.partial + ((size_t)g.slot * 2 * kT + x * kT + r) * kPartial<D>;
 #pragma unroll
         for (int j = 0; j < D / 32; ++j) {
           uint32_t o[32];
@@ -864,13 +865,12 @@ do {                                                                            
 
 // Joins the partial sums of units that the line's cuts run through: blocks
 // (i, y) stand for cut i + 1, and share the unit's rows with the blocks of its
-// other cuts.  A warp takes a row; the order of the sum is the pieces'.
+// other cuts.
 template <int D>
-__global__ void __launch_bounds__(256) s2_cache_chunk_join_kernel(const __grid_constant__ CacheArgs c,
-                                                                  const __grid_constant__ AttnIn in) {
+__global__ void __launch_bounds__(kJoinThreads) s2_cache_chunk_join_kernel(const __grid_constant__ CacheArgs c,
+                                                                           const __grid_constant__ AttnIn in) {
   using namespace chunk;
-  constexpr int kThreads = 256;
-  __shared__ long long sh[kThreads / 32 + 2];
+  __shared__ JoinShared<D> sh;
   const int per_tile = kT / in.g;
   auto weight_of = [&](int b) -> long long {
     const Seq s = load_seq(c, b);
@@ -878,7 +878,8 @@ __global__ void __launch_bounds__(256) s2_cache_chunk_join_kernel(const __grid_c
   };
   int b;
   long long start;
-  const Line line = find_piece<kThreads>(c.B, in.pieces, in.min_piece, blockIdx.x + 1, sh, weight_of, b, start);
+  const Line line =
+      find_piece<kJoinThreads>(c.B, in.pieces, in.min_piece, blockIdx.x + 1, sh.line, weight_of, b, start);
   const long long cut = line.piece * (blockIdx.x + 1);
   if (cut >= line.total) return;
   const Seq s = load_seq(c, b);
@@ -888,52 +889,20 @@ __global__ void __launch_bounds__(256) s2_cache_chunk_join_kernel(const __grid_c
   const long long begin = start + h * u.head() + u.before(j), w = u.weight(j);
   if (begin == cut) return;
   const int tiles = pair_tiles(s, u, j);
-  if (tiles == 0) return;
   const int p0 = (int)(begin / line.piece), p1 = (int)((begin + w - 1) / line.piece);
-  auto first_tile = [&](int p) { return tile_at(tiles, max(line.piece * p, begin) - begin, w); };
-  auto end_tile = [&](int p) { return tile_at(tiles, min(line.piece * (p + 1), begin + w) - begin, w); };
+  // pieces between hold tiles (a piece is many tiles long); the first and the last may hold none
+  const int q0 = p0 + (tile_at(tiles, line.piece * (p0 + 1) - begin, w) == 0);
+  const int q1 = p1 - (tile_at(tiles, line.piece * p1 - begin, w) == tiles);
+  if (q0 >= q1) return;  // one piece had all of the unit's tiles and wrote its rows
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int left = s.n - j * u.d;
-  const int workers = (p1 - p0) * gridDim.y * (kThreads / 32);
-  const int me = (((int)blockIdx.x - p0) * gridDim.y + blockIdx.y) * (kThreads / 32) + warp;
-  constexpr int kV = D / 32;  // channels of a lane
-  for (int i = me; i < min(left, u.d) * in.g; i += workers) {
-    const int tok = i / in.g, head = i % in.g;
-    const int row = (tok / per_tile) * kT + (tok % per_tile) * in.g + head;
-    float mm = -INFINITY, ll = 0.f, o[kV] = {};
-    for (int p = p0; p <= p1; ++p) {
-      const int ta = first_tile(p), tb = end_tile(p);
-      if (ta == tb) continue;
-      if (ta == 0 && tb == tiles) return;  // one piece had all of the unit's tiles and wrote its rows
-      const float* part =
-          in.partial + ((size_t)(2 * p + (begin <= line.piece * p ? 0 : 1)) * 2 * kT + row) * (D + 4);
-      const float2 ml = *reinterpret_cast<const float2*>(part + D);
-      float v[kV];
-      if constexpr (kV == 4) {
-        const float4 t = *reinterpret_cast<const float4*>(part + 4 * lane);
-        v[0] = t.x, v[1] = t.y, v[2] = t.z, v[3] = t.w;
-      } else {
-        const float2 t = *reinterpret_cast<const float2*>(part + 2 * lane);
-        v[0] = t.x, v[1] = t.y;
-      }
-      if (ml.x == -INFINITY) continue;
-      const float m = fmaxf(mm, ml.x);
-      const float f0 = ex2(mm - m), f1 = ex2(ml.x - m);
-      ll = ll * f0 + ml.y * f1;
-#pragma unroll
-      for (int z = 0; z < kV; ++z) o[z] = o[z] * f0 + v[z] * f1;
-      mm = m;
-    }
-    const float inv = ll > 0.f ? 1.f / ll : 0.f;
-    const size_t out = (size_t)(s.first + j * u.d + tok) * in.heads + h * in.g + head;
-    uint32_t* dst = reinterpret_cast<uint32_t*>(in.o + out * D) + lane * (kV / 2);
-    if constexpr (kV == 4)
-      *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv));
-    else
-      *dst = pack_bf16(o[0] * inv, o[1] * inv);
-    if (in.lse && lane == 0) in.lse[out] = ll > 0.f ? (mm + log2f(ll)) * 0.69314718055994531f : -INFINITY;
-  }
+  join_rows<D>(
+      sh, min(s.n - j * u.d, u.d) * in.g, ((int)blockIdx.x - p0) * gridDim.y + blockIdx.y, (p1 - p0) * gridDim.y, q0,
+      q1,
+      [&](int p, int i) {
+        const int tok = i / in.g, row = (tok / per_tile) * kT + (tok % per_tile) * in.g + i % in.g;
+        return in.partial + ((size_t)(2 * p + (begin <= line.piece * p ? 0 : 1)) * 2 * kT + row) * kPartial<D>;
+      },
+      [&](int i) { return (size_t)(s.first + j * u.d + i / in.g) * in.heads + h * in.g + i % in.g; }, in.o, in.lse);
 }
 
 template <int D, bool Q4>
@@ -948,8 +917,8 @@ static int chunk_impl(const CUtensorMap* tq, const CUtensorMap* tk, const CUtens
   e = cudaGetLastError();
   if (e != cudaSuccess) return (int)e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(in.pieces - 1, 4);
-  cfg.blockDim = dim3(256);
+  cfg.gridDim = dim3(in.pieces - 1, 8);
+  cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = stream;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -1,0 +1,124 @@
+// s2_cache_join.cuh -- adding up the partial sums of a unit of cached attention
+// that several CTAs computed (s2_cache_attn.cu, s2_cache_chunk.cu).
+//
+// A piece leaves for each row O (D floats, not divided), then its maximum
+// score and sum of weights; in the order of the pieces
+//     m = max m_p,  o = sum 2^(m_p - m) O_p / sum 2^(m_p - m) l_p.
+// What bounds it is the latency of reading them, so all of a warp's loads are
+// asked for before the first is used: with up to 8 pieces a warp takes a row,
+// with more a CTA does, its warps sharing the pieces.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "sm100_ptx.cuh"
+
+namespace s2 {
+
+constexpr int kJoinThreads = 256;
+constexpr int kJoinBatch = 8;  // pieces that a warp asks for at once
+
+// Floats of a row's partial sums.
+template <int D>
+constexpr int kPartial = D + 4;
+
+template <int D>
+struct JoinShared {
+  long long line[kJoinThreads / 32 + 2];
+  float m[kJoinThreads / 32], l[kJoinThreads / 32];
+  float o[kJoinThreads / 32][D];
+};
+
+// Sum of pieces p, p + by, .. <= p1 of one row: a lane holds channels [lane·D/32, ..).
+template <int D, typename Part>
+__device__ __forceinline__ void join_pieces(int p, int by, int p1, int row, Part part, float& m, float& l,
+                                            float (&o)[D / 32]) {
+  constexpr int kV = D / 32;
+  const int lane = threadIdx.x % 32;
+  m = -INFINITY;
+  l = 0.f;
+#pragma unroll
+  for (int z = 0; z < kV; ++z) o[z] = 0.f;
+  for (; p <= p1; p += kJoinBatch * by) {
+    float2 ml[kJoinBatch];
+    float v[kJoinBatch][kV];
+#pragma unroll
+    for (int i = 0; i < kJoinBatch; ++i) {
+      ml[i] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+      for (int z = 0; z < kV; ++z) v[i][z] = 0.f;
+      if (p + i * by <= p1) {
+        const float* from = part(p + i * by, row);
+        ml[i] = *reinterpret_cast<const float2*>(from + D);
+        if constexpr (kV == 4) {
+          const float4 t = *reinterpret_cast<const float4*>(from + 4 * lane);
+          v[i][0] = t.x, v[i][1] = t.y, v[i][2] = t.z, v[i][3] = t.w;
+        } else {
+          const float2 t = *reinterpret_cast<const float2*>(from + 2 * lane);
+          v[i][0] = t.x, v[i][1] = t.y;
+        }
+      }
+    }
+    float top = m;
+#pragma unroll
+    for (int i = 0; i < kJoinBatch; ++i) top = fmaxf(top, ml[i].x);
+    if (top == -INFINITY) continue;
+    const float f = ex2(m - top);
+    l *= f;
+#pragma unroll
+    for (int z = 0; z < kV; ++z) o[z] *= f;
+#pragma unroll
+    for (int i = 0; i < kJoinBatch; ++i) {
+      const float g = ex2(ml[i].x - top);
+      l = fmaf(ml[i].y, g, l);
+#pragma unroll
+      for (int z = 0; z < kV; ++z) o[z] = fmaf(v[i][z], g, o[z]);
+    }
+    m = top;
+  }
+}
+
+// Rows of a unit whose pieces are p0..p1, shared out over `helpers` CTAs (this one is `nth`).
+// part(p, row): a row's partial sums of piece p; out(row): its number in o and lse.
+template <int D, typename Part, typename Out>
+__device__ __forceinline__ void join_rows(JoinShared<D>& sh, int rows, int nth, int helpers, int p0, int p1, Part part,
+                                          Out out, __nv_bfloat16* o_all, float* lse) {
+  constexpr int kW = kJoinThreads / 32, kV = D / 32;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const bool narrow = p1 - p0 < kJoinBatch;
+  const int first = narrow ? nth * kW + warp : nth, by = narrow ? helpers * kW : helpers;
+  for (int row = first; row < rows; row += by) {
+    float m, l, o[kV];
+    join_pieces<D>(narrow ? p0 : p0 + warp, narrow ? 1 : kW, p1, row, part, m, l, o);
+    if (!narrow) {
+      __syncthreads();
+      if (lane == 0) sh.m[warp] = m, sh.l[warp] = l;
+#pragma unroll
+      for (int z = 0; z < kV; ++z) sh.o[warp][kV * lane + z] = o[z];
+      __syncthreads();
+      if (warp != 0) continue;
+#pragma unroll
+      for (int w = 1; w < kW; ++w) m = fmaxf(m, sh.m[w]);
+      l = 0.f;
+#pragma unroll
+      for (int z = 0; z < kV; ++z) o[z] = 0.f;
+#pragma unroll
+      for (int w = 0; w < kW; ++w) {
+        const float f = m == -INFINITY ? 0.f : ex2(sh.m[w] - m);
+        l = fmaf(sh.l[w], f, l);
+#pragma unroll
+        for (int z = 0; z < kV; ++z) o[z] = fmaf(sh.o[w][kV * lane + z], f, o[z]);
+      }
+    }
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const size_t at = out(row);
+    uint32_t* dst = reinterpret_cast<uint32_t*>(o_all + at * D) + lane * (kV / 2);
+    if constexpr (kV == 4)
+      *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv));
+    else
+      *dst = pack_bf16(o[0] * inv, o[1] * inv);
+    if (lse && lane == 0) lse[at] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+  }
+}
+
+}  // namespace s2
