@@ -303,22 +303,36 @@ __global__ void __launch_bounds__(W * 32, ctas_per_sm<NR, W>())
 
     KeyRegs<D, Q4> kr[kBlocks];
     ValueRegs<D, Q4> vr[kBlocks];
-    size_t rows[kBlocks];  // first rows of the next step's blocks
+    uint32_t rows[kBlocks];  // first rows of the next step's blocks (a cache's rows are counted in 32 bits)
     int k = k0 + warp;
+    const int* const pages = c.table + (size_t)b * c.width;
+    const int last_block = (seq.len - 1) & ~15, slot_mask = (1 << c.log2s) - 1;
+    auto find_row = [&](int p) -> uint32_t {
+      int page = pages[p >> c.log2s];
+      if ((uint32_t)page >= (uint32_t)c.pages) {
+        atomicOr(c.status, kCacheFlag);
+        page = 0;
+      }
+      return ((((uint32_t)page * (uint32_t)c.heads + (uint32_t)h) << c.log2s)) + (uint32_t)(p & slot_mask);
+    };
     // a block behind the last key is read from the last block instead: it lies in a page of the sequence
     auto find_rows = [&](int step) {
+      rows[0] = find_row(step * kStep);
 #pragma unroll
-      for (int u = 0; u < kBlocks; ++u) {
-        const int p = min(step * kStep + 16 * u, (seq.len - 1) & ~15);
-        rows[u] = row_of(c, page_of(c, b, p), h, p);
+      for (int u = 1; u < kBlocks; ++u) {
+        const int p = step * kStep + 16 * u;
+        if (p > last_block)
+          rows[u] = rows[u - 1];
+        else
+          rows[u] = c.log2s >= 5 && u % 2 ? rows[u - 1] + 16 : find_row(p);  // pages of 32 rows hold two blocks
       }
     };
     if (seq.len > 0 && k < k1) {
       find_rows(k);
 #pragma unroll
-      for (int u = 0; u < kBlocks; ++u) load_keys(kr[u], k_base + rows[u] * kRowBytes, ks_base + rows[u] * 4);
+      for (int u = 0; u < kBlocks; ++u) load_keys(kr[u], k_base + (size_t)rows[u] * kRowBytes, ks_base + (size_t)rows[u] * 4);
 #pragma unroll
-      for (int u = 0; u < kBlocks; ++u) load_values(vr[u], v_base + rows[u] * kRowBytes, vs_base + rows[u] * 4);
+      for (int u = 0; u < kBlocks; ++u) load_values(vr[u], v_base + (size_t)rows[u] * kRowBytes, vs_base + (size_t)rows[u] * 4);
       for (; k < k1; k += W) {
         const int key0 = k * kStep;
         const bool more = k + W < k1;
@@ -370,7 +384,7 @@ __global__ void __launch_bounds__(W * 32, ctas_per_sm<NR, W>())
         }
         if (more) {
 #pragma unroll
-          for (int u = 0; u < kBlocks; ++u) load_keys(kr[u], k_base + rows[u] * kRowBytes, ks_base + rows[u] * 4);
+          for (int u = 0; u < kBlocks; ++u) load_keys(kr[u], k_base + (size_t)rows[u] * kRowBytes, ks_base + (size_t)rows[u] * 4);
         }
         // masks, only where some row or the sequence ends in the step
         if (key0 + kStep > lim_all) {
@@ -493,7 +507,7 @@ __global__ void __launch_bounds__(W * 32, ctas_per_sm<NR, W>())
         }
         if (more) {
 #pragma unroll
-          for (int u = 0; u < kBlocks; ++u) load_values(vr[u], v_base + rows[u] * kRowBytes, vs_base + rows[u] * 4);
+          for (int u = 0; u < kBlocks; ++u) load_values(vr[u], v_base + (size_t)rows[u] * kRowBytes, vs_base + (size_t)rows[u] * 4);
         }
       }
     }

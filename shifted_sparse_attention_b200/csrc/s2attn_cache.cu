@@ -28,6 +28,8 @@ int take(const s2_cache* cache, const s2_cache_batch* batch, s2::CacheArgs* a) {
     return report_error(S2_ERR_UNSUPPORTED, "page_size=%lld: pages hold 16, 32, 64 or 128 rows", (long long)S);
   if (cache->heads > 65535 || cache->pages >= (int64_t(1) << 31) || cache->pages * cache->heads >= (int64_t(1) << 31))
     return report_error(S2_ERR_UNSUPPORTED, "pages*heads must be below 2^31 and heads below 65536");
+  if (cache->pages * cache->heads >= (int64_t(1) << 32) / S)
+    return report_error(S2_ERR_UNSUPPORTED, "pages*heads*page_size must be below 2^32");
   if (batch->seqs < 1 || batch->tokens < 1 || batch->table_width < 1)
     return report_error(S2_ERR_SHAPE, "seqs, tokens and table_width must be positive");
   if (batch->max_new < 0 || batch->max_new > batch->tokens)
@@ -95,8 +97,15 @@ int64_t shared_rows(const s2_cache* cache, const s2_cache_batch* batch, int64_t 
   return n * (heads / cache->heads);
 }
 
-// Up to this many, the cache's bytes bound the call (s2_cache_attn.cu); beyond, the products (s2_cache_chunk.cu).
-constexpr int64_t kFewRows = 32;
+// Whether the call's bytes bound it (s2_cache_attn.cu: a key is read, and unpacked, once for every 16 query rows) or
+// its products (s2_cache_chunk.cu: 128 rows at a time, at 20 to 40 us for the first tile).  One block of rows is the
+// former's always.  Beyond, measured on bf16 rows of 128 channels, us of one and the other: 1 x 30000 keys, 8 heads,
+// 64 rows (10^6 keys times blocks) 59 and 53; 16 x 4000, 32 rows (10^6) 62 and 63, 64 rows (2·10^6) 114 and 68;
+// 1 x 2000, 1 head, 128 rows (16·10^3) 11 and 34.
+bool few_rows(const s2_cache* cache, const s2_cache_batch* batch, int64_t heads) {
+  const int64_t rows = shared_rows(cache, batch, heads), len = batch->max_len ? batch->max_len : batch->table_width * cache->page_size;
+  return rows <= 16 || (double)batch->seqs * (double)len * (double)cache->heads * (double)((rows + 15) / 16) <= 1e6;
+}
 
 int launched(int rc, const char* what) {
   if (rc == 0) return S2_OK;
@@ -167,8 +176,8 @@ int s2attn_cache_read(const s2_cache* cache, const s2_cache_batch* batch, void* 
 size_t s2attn_cache_attn_workspace_size(const s2_cache* cache, const s2_cache_batch* batch, int64_t heads) {
   s2::CacheArgs a;
   if (take(cache, batch, &a) != S2_OK || check_heads(cache, heads) != S2_OK) return 0;
-  return shared_rows(cache, batch, heads) <= kFewRows ? s2::cache_decode_partial_bytes((int)cache->D)
-                                                      : s2::cache_chunk_partial_bytes((int)cache->D);
+  return few_rows(cache, batch, heads) ? s2::cache_decode_partial_bytes((int)cache->D)
+                                       : s2::cache_chunk_partial_bytes((int)cache->D);
 }
 
 int s2attn_cache_attn(const s2_cache* cache, const s2_cache_batch* batch, const void* q, int64_t ldq, void* o,
@@ -199,16 +208,14 @@ int s2attn_cache_attn(const s2_cache* cache, const s2_cache_batch* batch, const 
   in.g = (int)(heads / cache->heads);
   in.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)D));
   const bool q4 = cache->format == S2_CACHE_Q4;
-  const int64_t rows = shared_rows(cache, batch, heads);
-  if (rows <= kFewRows) {
-    in.pieces = s2::kDecodePieces;
-    in.min_piece = 16;
+  if (few_rows(cache, batch, heads)) {
+    const int64_t rows = shared_rows(cache, batch, heads);
     return launched(s2::launch_cache_decode(a, in, (int)D, q4, rows > 16 ? 16 : (int)rows,
                                             static_cast<cudaStream_t>(stream)),
                     "cache attention");
   }
   in.pieces = s2::kChunkPieces;
-  in.min_piece = 2048;  // keys: less is not worth a second launch's reading of partial sums
+  in.min_piece = 1024;  // keys: less is not worth a second launch's reading of partial sums
   const uint64_t S = (uint64_t)cache->page_size, d = (uint64_t)D, blocks = (uint64_t)(cache->pages * cache->heads);
   CUtensorMap tq, tk, tv;
   if ((rc = s2::encode_map(&tq, q, {d, (uint64_t)heads, (uint64_t)batch->tokens}, {d * 2, (uint64_t)ldq * 2},

@@ -19,19 +19,24 @@ def on_gpu(c):
     return s2.KVCache(*[t.cuda() for t in (c.k, c.v, c.ks, c.vs) if t is not None])
 
 
-def batch_of(c, news, plain=False, extra=0, **hints):
+def batch_of(c, news, plain=False, extra=0, wide=False, **hints):
+    """wide: a table with room for a million keys, which the call then has to reckon with (it takes the kernel for
+    many rows, whatever the lengths are)."""
     lens = torch.tensor(c.lens, dtype=torch.int32).cuda()
     starts = None if plain else starts_of(news).cuda()
-    return s2.CacheBatch(c.table.cuda(), lens, starts, sum(news) + extra, **hints)
+    table = c.table
+    if wide:
+        table = torch.nn.functional.pad(table, (0, (1 << 20) // c.S), value=-7)
+    return s2.CacheBatch(table.cuda(), lens, starts, sum(news) + extra, **hints)
 
 
-def check_attention(c, news, H, seed=0, plain=False, **hints):
+def check_attention(c, news, H, seed=0, plain=False, wide=False, **hints):
     T = sum(news)
     g = torch.Generator().manual_seed(seed)
     q = torch.randn(T, H, c.dim, generator=g).bfloat16()
     o, lse, to, tl = ref.attention(c, q, starts_of(news))
     got_lse = torch.empty(T, H, device="cuda")
-    got = s2.cache_attention(on_gpu(c), batch_of(c, news, plain, **hints), q.cuda(), lse=got_lse)
+    got = s2.cache_attention(on_gpu(c), batch_of(c, news, plain, wide=wide, **hints), q.cuda(), lse=got_lse)
     s2.check_status()
     got, got_lse = got.double().cpu(), got_lse.double().cpu()
     assert torch.isfinite(got).all()
@@ -73,6 +78,7 @@ def test_heads_shared_by_key_heads(bits, D, H, Hkv):
     check_attention(c, [3, 2], H, max_new=3)
 
 
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("bits", [16, 4])
 @pytest.mark.parametrize("D,H,Hkv,S", [(128, 4, 2, 128), (64, 6, 2, 16), (128, 5, 1, 64)])
 @pytest.mark.parametrize("lens,news", [
@@ -81,18 +87,36 @@ def test_heads_shared_by_key_heads(bits, D, H, Hkv):
     ([640, 64, 1], [256, 64, 1]),   # chunks beside a single token
     ([1200], [700]),
 ])
-def test_chunks_of_prompts(bits, D, H, Hkv, S, lens, news):
+def test_chunks_of_prompts(bits, D, H, Hkv, S, lens, news, wide):
     c = ref.Paged(lens, Hkv, D, S, bits, seed=lens[0])
-    check_attention(c, news, H, max_new=max(news), max_len=max(lens))
+    check_attention(c, news, H, wide=wide, max_new=max(news), max_len=0 if wide else max(lens))
 
 
 @pytest.mark.parametrize("bits", [16, 4])
-@pytest.mark.parametrize("max_new", [1, 0])
-def test_rows_that_see_nothing_and_sequences_left_out(bits, max_new):
+@pytest.mark.parametrize("lens,news", [
+    ([9000], [300]),                            # units cut over several CTAs
+    ([2500, 700, 31, 4000], [64, 700, 31, 5]),
+    ([128, 256, 384] * 12, [128, 1, 300] * 12),  # many units for a CTA
+])
+def test_units_cut_over_ctas(bits, lens, news):
+    c = ref.Paged(lens, 2, 128, 64, bits, seed=lens[0])
+    check_attention(c, news, 6, wide=True, max_new=max(news))
+
+
+@pytest.mark.parametrize("bits", [16, 4])
+@pytest.mark.parametrize("H,Hkv", [(8, 1), (3, 3), (7, 1), (128, 1), (48, 2), (20, 4)])
+def test_chunks_with_heads_shared_by_key_heads(bits, H, Hkv):
+    c = ref.Paged([333, 150], Hkv, 64, 32, bits, seed=H)
+    check_attention(c, [40, 150], H, wide=True, max_new=150)
+
+
+@pytest.mark.parametrize("bits", [16, 4])
+@pytest.mark.parametrize("max_new,wide", [(1, False), (0, False), (5, True)])
+def test_rows_that_see_nothing_and_sequences_left_out(bits, max_new, wide):
     # lengths of zero (a padded batch), fewer rows than new tokens, no new token
     lens, news = [0, 40, 2, 300, 0], [1, 1, 5, 0, 3]
     c = ref.Paged(lens, 2, 128, 16, bits)
-    got = check_attention(c, news, 4, max_new=max_new)
+    got = check_attention(c, news, 8, wide=wide, max_new=max_new)
     assert (got[0] == 0).all() and (got[2:5] == 0).all() and (got[5] != 0).any()
 
 
@@ -101,19 +125,23 @@ def test_hints_change_no_result_and_runs_repeat_bitwise(max_new):
     lens, news = [1500, 260, 77], [1, 200, 3]
     c = ref.Paged(lens, 2, 128, 64, 16)
     a = check_attention(c, news, 8, max_new=max_new)
-    b = check_attention(c, news, 8, max_new=max_new, max_len=1500)
+    b = check_attention(c, news, 8, wide=True, max_new=200)
     assert torch.equal(a, check_attention(c, news, 8, max_new=max_new)) and (a - b).abs().max() < 2e-2
+    assert torch.equal(b, check_attention(c, news, 8, wide=True, max_new=200))
 
 
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("bits", [16, 4])
-def test_tokens_of_no_sequence_are_left_as_they_were(bits):
+def test_tokens_of_no_sequence_are_left_as_they_were(bits, wide):
     c = ref.Paged([90, 33], 2, 64, 16, bits)
     news, extra, before = [2, 1], 4, 3
     T = sum(news) + extra + before
     starts = (starts_of(news) + before).to(torch.int32).cuda()
-    batch = s2.CacheBatch(c.table.cuda(), torch.tensor(c.lens, dtype=torch.int32).cuda(), starts, T, max_new=2)
-    q = torch.randn(T, 4, 64).bfloat16().cuda()
-    out, lse = torch.full((T, 4, 64), 7.0).bfloat16().cuda(), torch.full((T, 4), 7.0).cuda()
+    table = torch.nn.functional.pad(c.table, (0, 1 << 16), value=-7) if wide else c.table
+    batch = s2.CacheBatch(table.cuda(), torch.tensor(c.lens, dtype=torch.int32).cuda(), starts, T, max_new=T)
+    H = 32 if wide else 4
+    q = torch.randn(T, H, 64).bfloat16().cuda()
+    out, lse = torch.full((T, H, 64), 7.0).bfloat16().cuda(), torch.full((T, H), 7.0).cuda()
     s2.cache_attention(on_gpu(c), batch, q, out=out, lse=lse)
     rows = [torch.full((T, 2, 64), 7.0).bfloat16().cuda() for _ in range(2)]
     s2.cache_read(on_gpu(c), batch, out=rows)
@@ -168,7 +196,8 @@ def test_rows_beyond_32_bit_offsets():
         starts = starts_of(news)
         q = torch.randn(sum(news), 4, D).bfloat16()
         o, _, to, _ = ref.attention(c, q, starts)
-        batch = s2.CacheBatch(table, lens, starts.cuda(), sum(news), max_new=max(news))
+        wide = torch.nn.functional.pad(table, (0, 1 << 13), value=-7) if max(news) > 1 else table
+        batch = s2.CacheBatch(wide.contiguous(), lens, starts.cuda(), sum(news), max_new=max(news))
         got = s2.cache_attention(cache, batch, q.cuda())
         assert ((got.double().cpu() - o).abs() <= to).all()
     k, _ = s2.cache_read(cache, batch)
