@@ -180,19 +180,20 @@ __device__ __forceinline__ long long seq_steps(const CacheArgs& c, const AttnIn&
 template <bool Q4>
 __host__ __device__ constexpr int step_blocks() { return Q4 ? 2 : 1; }
 
-// CTAs of W warps on an SM: 16 warps of 128 registers, 8 of 255 with two blocks of query rows.
-template <int NR, int W>
-__host__ __device__ constexpr int ctas_per_sm() { return (NR == 1 ? 16 : 8) / W; }
+// CTAs of W warps on an SM: 12 warps of 168 registers for bf16 rows (16 of 128 spill: one sequence of 32768 keys took
+// 28.7 us and not 23.1), 16 of 128 for 4-bit ones, 8 of 255 with two blocks of query rows.
+template <bool Q4, int NR, int W>
+__host__ __device__ constexpr int ctas_per_sm() { return (NR == 2 ? 8 : Q4 ? 16 : 12) / W; }
 
 template <int D, int NR, int W>
 struct DecodeShared {
   long long line[W + 2];
   float m[W][8 * NR], l[W][8 * NR];
-  float o[W][8 * NR][D + 4];
+  alignas(16) float o[W][8 * NR][D + 4];
 };
 
 template <int D, bool Q4, int NR, int W>
-__global__ void __launch_bounds__(W * 32, ctas_per_sm<NR, W>())
+__global__ void __launch_bounds__(W * 32, ctas_per_sm<Q4, NR, W>())
     s2_cache_decode_kernel(const __grid_constant__ CacheArgs c, const __grid_constant__ AttnIn in) {
   constexpr int kThreads = W * 32;
   constexpr int kBlocks = step_blocks<Q4>();
@@ -606,7 +607,7 @@ __global__ void __launch_bounds__(kJoinThreads) s2_cache_join_kernel(const __gri
 template <int D, bool Q4, int NR, int W>
 static int decode_impl(const CacheArgs& c, const AttnIn& in0, cudaStream_t stream) {
   AttnIn in = in0;
-  in.pieces = 148 * ctas_per_sm<NR, W>();
+  in.pieces = 148 * ctas_per_sm<Q4, NR, W>();
   in.min_piece = unit_steps<W>() + W;  // a step for each warp
   constexpr int kBytes = (int)sizeof(DecodeShared<D, NR, W>);
   cudaError_t e;

@@ -26,7 +26,7 @@ template <int D>
 struct JoinShared {
   long long line[kJoinThreads / 32 + 2];
   float m[kJoinThreads / 32], l[kJoinThreads / 32];
-  float o[kJoinThreads / 32][D];
+  alignas(16) float o[kJoinThreads / 32][D];
 };
 
 // Sum of pieces p, p + by, .. <= p1 of one row: a lane holds channels [lane·D/32, ..).
