@@ -21,8 +21,11 @@ import torch
 from . import binding
 from .binding import _check, _ptr, lib
 
-# the current stream's handle without the object around it: a step's calls are short enough for that to count
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+# The current stream's handle without the object around it, and the current device: a step's calls are short enough
+# for the host's time to count (the helpers below look at each tensor once and pass plain numbers on).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda device: torch.cuda.current_stream(device).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 CACHE_BF16, CACHE_Q4 = 0, 1
 
@@ -59,7 +62,7 @@ class KVCache:
         self.pages, self.heads, self.page_size = (int(x) for x in k.shape[:3])
         self.dim = int(k.shape[3]) * (2 if q4 else 1)
         self.format = CACHE_Q4 if q4 else CACHE_BF16
-        self.device = k.device
+        self.device, self.index = k.device, k.device.index
         self._struct = _CacheStruct(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), self.pages, self.heads,
                                     self.page_size, self.dim, self.format)
         self.address = ctypes.addressof(self._struct)
@@ -98,16 +101,14 @@ class CacheBatch:
                 raise ValueError("with q_starts, tokens (the length of the packed axis) must be given")
             tokens = seqs
         self.page_table, self.seq_lens, self.q_starts = page_table, seq_lens, q_starts
-        self.seqs, self.tokens, self.device = seqs, int(tokens), page_table.device
+        self.seqs, self.tokens, self.index = seqs, int(tokens), page_table.device.index
         self._struct = _BatchStruct(_ptr(page_table), _ptr(seq_lens), _ptr(q_starts), seqs, self.tokens, width,
                                     int(max_new), int(max_len))
         self.address = ctypes.addressof(self._struct)
 
 
 def _stream(stream, cache) -> int:
-    if stream is None and _raw_stream is not None:
-        return _raw_stream(cache.device.index)
-    return binding._stream(stream)
+    return _raw_stream(cache.index) if stream is None else binding._stream(stream)
 
 
 # ------------------------------------------------------------------ raw entry points (same names as the C ABI)
@@ -146,18 +147,20 @@ def _on(device, stream):
                 yield
 
 
-def _plain(cache, stream):
-    """Nothing to switch: the call runs on the current stream of the cache's device."""
-    return stream is None and cache.device.index == torch.cuda.current_device()
+def _plain(cache, batch, stream):
+    """Whether there is nothing to switch: the call runs on the current stream of the cache's device."""
+    if batch.index != cache.index:
+        raise ValueError("the batch is on another device than the cache")
+    return stream is None and cache.index == _current_device()
 
 
 def _rows(name, t, cache, batch, heads):
     """Row stride of [tokens, heads, D] bf16 rows whose heads lie side by side."""
-    if t.dtype != torch.bfloat16 or t.device != cache.device or t.shape != (batch.tokens, heads, cache.dim):
+    if t.dtype is not torch.bfloat16 or t.get_device() != cache.index or t.shape != (batch.tokens, heads, cache.dim):
         raise ValueError("%s must be bf16 [%d, %d, %d] on the cache's device" % (
             name, batch.tokens, heads, cache.dim))
     row, head, one = t.stride()
-    if one != 1 or (heads > 1 and head != cache.dim):
+    if one != 1 or (head != cache.dim and heads > 1):
         raise ValueError("the heads of a token of %s must lie side by side" % name)
     return row if batch.tokens > 1 else max(row, heads * cache.dim)
 
@@ -168,13 +171,8 @@ def _query_heads(q):
     return q.shape[1]
 
 
-def _same_device(cache, batch):
-    if batch.device != cache.device:
-        raise ValueError("the batch is on another device than the cache")
-
-
 def _whole(name, t, shape, cache, dtype=torch.bfloat16):
-    if t.shape != shape or t.dtype != dtype or t.device != cache.device or not t.is_contiguous():
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != cache.index or not t.is_contiguous():
         raise ValueError("%s must be a contiguous %s tensor %s on the cache's device" % (name, dtype, tuple(shape)))
 
 
@@ -182,10 +180,9 @@ def cache_append(cache: KVCache, batch: CacheBatch, k, v, q=None, positions=None
                  scale: float = 1.0, out=None, stream=None):
     """Stores the new tokens' keys (rotated to their positions) and values [tokens, cache.heads, D]; returns the
     rotated queries if q [tokens, heads, D] is given.  base=0: the keys are stored as they are."""
-    if not _plain(cache, stream):
+    if not _plain(cache, batch, stream):
         with _on(cache.device, stream):
             return cache_append(cache, batch, k, v, q, positions, base, scale, out)
-    _same_device(cache, batch)
     ldk, ldv = _rows("k", k, cache, batch, cache.heads), _rows("v", v, cache, batch, cache.heads)
     ldq = heads = 0
     if q is not None:
@@ -199,17 +196,19 @@ def cache_append(cache: KVCache, batch: CacheBatch, k, v, q=None, positions=None
         raise ValueError("out goes with q")
     if positions is not None:
         _whole("positions", positions, (batch.tokens,), cache, torch.int32)
-    _check(s2attn_cache_append(cache, batch, q, ldq, k, ldk, v, ldv, out, heads, positions, float(base), float(scale)))
+    _check(lib().s2attn_cache_append(
+        cache.address, batch.address, None if q is None else q.data_ptr(), ldq, k.data_ptr(), ldk, v.data_ptr(), ldv,
+        None if q is None else out.data_ptr(), heads, None if positions is None else positions.data_ptr(), base, scale,
+        _raw_stream(cache.index)))
     return out
 
 
 def cache_read(cache: KVCache, batch: CacheBatch, out=None, stream=None):
     """The rows of the batch's new tokens back as bf16 (k, v) [tokens, cache.heads, D]; tokens without a row are left
     as they were in ``out``, an optional preallocated pair."""
-    if not _plain(cache, stream):
+    if not _plain(cache, batch, stream):
         with _on(cache.device, stream):
             return cache_read(cache, batch, out)
-    _same_device(cache, batch)
     shape = (batch.tokens, cache.heads, cache.dim)
     if out is None:
         k, v = (torch.empty(shape, dtype=torch.bfloat16, device=cache.device) for _ in range(2))
@@ -217,7 +216,7 @@ def cache_read(cache: KVCache, batch: CacheBatch, out=None, stream=None):
         k, v = out
         _whole("out", k, shape, cache)
         _whole("out", v, shape, cache)
-    _check(s2attn_cache_read(cache, batch, k, v))
+    _check(lib().s2attn_cache_read(cache.address, batch.address, k.data_ptr(), v.data_ptr(), _raw_stream(cache.index)))
     return k, v
 
 
@@ -233,10 +232,9 @@ def cache_attention_workspace(cache: KVCache, batch: CacheBatch, heads: int):
 def cache_attention(cache: KVCache, batch: CacheBatch, q, out=None, lse=None, workspace=None, stream=None):
     """Attention of the new tokens' queries [tokens, heads, D] (rotated) over their sequences up to themselves; returns
     o [tokens, heads, D].  lse: optional float32 [tokens, heads] to fill.  Without a workspace one is allocated."""
-    if not _plain(cache, stream):
+    if not _plain(cache, batch, stream):
         with _on(cache.device, stream):
             return cache_attention(cache, batch, q, out, lse, workspace)
-    _same_device(cache, batch)
     heads = _query_heads(q)
     ldq = _rows("q", q, cache, batch, heads)
     if out is None:
@@ -247,8 +245,9 @@ def cache_attention(cache: KVCache, batch: CacheBatch, q, out=None, lse=None, wo
         _whole("lse", lse, q.shape[:2], cache, torch.float32)
     if workspace is None:
         workspace = cache_attention_workspace(cache, batch, heads)
-    elif workspace.device != cache.device or not workspace.is_contiguous():
+    elif workspace.get_device() != cache.index or not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous on the cache's device")
-    _check(s2attn_cache_attn(cache, batch, q, ldq, out, lse, heads, workspace,
-                             workspace.numel() * workspace.element_size()))
+    _check(lib().s2attn_cache_attn(
+        cache.address, batch.address, q.data_ptr(), ldq, out.data_ptr(), None if lse is None else lse.data_ptr(), heads,
+        workspace.data_ptr(), workspace.nbytes, _raw_stream(cache.index)))
     return out

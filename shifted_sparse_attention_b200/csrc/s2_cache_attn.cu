@@ -30,6 +30,8 @@
 //   factor 256), which one vote per step tells; sums are in 32 bits, the
 //   weights are rounded to bf16 for the product (relative 2^-9 each, independent
 //   signs) and added up unrounded.
+#include <climits>
+
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -169,9 +171,9 @@ template <int W>
 __host__ __device__ constexpr int unit_steps() { return 2 * W; }
 
 template <int NR, int W>
-__device__ __forceinline__ long long seq_steps(const CacheArgs& c, const AttnIn& in, int b, int step) {
+__device__ __forceinline__ long long seq_steps(const CacheArgs& c, const AttnIn& in, int b, int step, bool cut) {
   const Seq s = load_seq(c, b);
-  return (long long)c.heads * row_blocks<NR>(s.n, in.g) * (steps_of(s.len, step) + unit_steps<W>());
+  return (long long)c.heads * row_blocks<NR>(s.n, in.g) * (cut ? steps_of(s.len, step) + unit_steps<W>() : 1);
 }
 
 }  // namespace
@@ -206,10 +208,13 @@ __global__ void __launch_bounds__(W * 32, ctas_per_sm<Q4, NR, W>())
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, r = lane / 4, cc = lane % 4;
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join may start its own set-up
-  auto weight = [&](int i) { return seq_steps<NR, W>(c, in, i, kStep); };
+  // cut units: each takes its steps of the line; whole units: one point each, and a CTA takes one unit
+  const bool cut = in.pieces > 0;
+  auto weight = [&](int i) { return seq_steps<NR, W>(c, in, i, kStep, cut); };
   int b;
   long long seq_first;
-  const Line line = find_piece<kThreads>(c.B, in.pieces, in.min_piece, blockIdx.x, sh.line, weight, b, seq_first);
+  const Line line = find_piece<kThreads>(c.B, cut ? in.pieces : INT_MAX, in.min_piece, blockIdx.x, sh.line, weight, b,
+                                         seq_first);
   const long long x0 = line.piece * blockIdx.x;
   if (x0 >= line.total) return;
   const long long x1 = min(x0 + line.piece, line.total);
@@ -224,18 +229,18 @@ __global__ void __launch_bounds__(W * 32, ctas_per_sm<Q4, NR, W>())
     Seq seq = load_seq(c, b);
     const int blocks = row_blocks<NR>(seq.n, in.g);
     const int steps = steps_of(seq.len, kStep);
-    const int span = steps + unit_steps<W>();
+    const int head = cut ? unit_steps<W>() : 0, span = cut ? steps + head : 1;
     if (x >= seq_first + (long long)c.heads * blocks * span) {  // this sequence is done
       seq_first += (long long)c.heads * blocks * span;
       ++b;
       continue;
     }
     const long long unit = (x - seq_first) / span;
-    const long long unit_first = seq_first + unit * span + unit_steps<W>();  // of its steps
+    const long long unit_first = seq_first + unit * span + head;  // of its steps
     const int h = (int)(unit / blocks), rb = (int)(unit % blocks);
     const int k0 = (int)max(0LL, x - unit_first);
-    const int k1 = (int)min((long long)steps, x1 - unit_first);
-    x = unit_first + steps;
+    const int k1 = cut ? (int)min((long long)steps, x1 - unit_first) : steps;
+    x = unit_first + (cut ? steps : 1);
     if (k1 <= k0) continue;
     const bool whole = k0 == 0 && k1 == steps;
 
@@ -325,7 +330,7 @@ __global__ void __launch_bounds__(W * 32, ctas_per_sm<Q4, NR, W>())
         if (p > last_block)
           rows[u] = rows[u - 1];
         else
-          rows[u] = c.log2s >= 5 && u % 2 ? rows[u - 1] + 16 : find_row(p);  // pages of 32 rows hold two blocks
+          rows[u] = c.log2s >= 5 && u % 2 ? rows[u - 1] + 16 : find_row(p);  // (steps of two blocks begin at even ones)
       }
     };
     if (seq.len > 0 && k < k1) {
@@ -577,7 +582,7 @@ __global__ void __launch_bounds__(kJoinThreads) s2_cache_join_kernel(const __gri
   constexpr int kStep = 16 * step_blocks<Q4>();
   constexpr int kRows = 8 * NR;
   __shared__ JoinShared<D> sh;
-  auto weight = [&](int i) { return seq_steps<NR, W>(c, in, i, kStep); };
+  auto weight = [&](int i) { return seq_steps<NR, W>(c, in, i, kStep, true); };
   int b;
   long long seq_first;
   const Line line =
@@ -605,19 +610,23 @@ __global__ void __launch_bounds__(kJoinThreads) s2_cache_join_kernel(const __gri
 }
 
 template <int D, bool Q4, int NR, int W>
-static int decode_impl(const CacheArgs& c, const AttnIn& in0, cudaStream_t stream) {
+static int decode_impl(const CacheArgs& c, const AttnIn& in0, bool cut, cudaStream_t stream) {
   AttnIn in = in0;
-  in.pieces = 148 * ctas_per_sm<Q4, NR, W>();
-  in.min_piece = unit_steps<W>() + W;  // a step for each warp
+  in.pieces = cut ? 148 * ctas_per_sm<Q4, NR, W>() : 0;
+  in.min_piece = cut ? unit_steps<W>() + W : 1;  // a step for each warp
   constexpr int kBytes = (int)sizeof(DecodeShared<D, NR, W>);
   cudaError_t e;
   if (kBytes > 48 * 1024) {
     e = cudaFuncSetAttribute(s2_cache_decode_kernel<D, Q4, NR, W>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
     if (e != cudaSuccess) return (int)e;
   }
-  s2_cache_decode_kernel<D, Q4, NR, W><<<in.pieces, W * 32, kBytes, stream>>>(c, in);
+  // units at most: every sequence rounds its rows up to blocks
+  const int64_t rows = (int64_t)c.T * in.g / (8 * NR) + (c.T < c.B ? c.T : c.B);
+  const int64_t units = c.heads * (c.starts ? rows : (int64_t)c.B * ((in.g + 8 * NR - 1) / (8 * NR)));
+  if (!cut && units >= (int64_t(1) << 31)) return (int)cudaErrorInvalidConfiguration;
+  s2_cache_decode_kernel<D, Q4, NR, W><<<(unsigned)(cut ? in.pieces : units), W * 32, kBytes, stream>>>(c, in);
   e = cudaGetLastError();
-  if (e != cudaSuccess) return (int)e;
+  if (e != cudaSuccess || !cut) return (int)e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(in.pieces - 1);
   cfg.blockDim = dim3(kJoinThreads);
@@ -631,13 +640,14 @@ static int decode_impl(const CacheArgs& c, const AttnIn& in0, cudaStream_t strea
 }
 
 template <int D, bool Q4>
-static int decode_rows(const CacheArgs& c, const AttnIn& in, int rows, cudaStream_t stream) {
-  return rows <= 8 ? decode_impl<D, Q4, 1, 4>(c, in, stream) : decode_impl<D, Q4, 2, 4>(c, in, stream);
+static int decode_rows(const CacheArgs& c, const AttnIn& in, int rows, bool cut, cudaStream_t stream) {
+  return rows <= 8 ? decode_impl<D, Q4, 1, 4>(c, in, cut, stream) : decode_impl<D, Q4, 2, 4>(c, in, cut, stream);
 }
 
-int launch_cache_decode(const CacheArgs& c, const AttnIn& in, int D, bool q4, int rows, cudaStream_t stream) {
-  if (D == 64) return q4 ? decode_rows<64, true>(c, in, rows, stream) : decode_rows<64, false>(c, in, rows, stream);
-  return q4 ? decode_rows<128, true>(c, in, rows, stream) : decode_rows<128, false>(c, in, rows, stream);
+int launch_cache_decode(const CacheArgs& c, const AttnIn& in, int D, bool q4, int rows, bool cut, cudaStream_t stream) {
+  if (D == 64)
+    return q4 ? decode_rows<64, true>(c, in, rows, cut, stream) : decode_rows<64, false>(c, in, rows, cut, stream);
+  return q4 ? decode_rows<128, true>(c, in, rows, cut, stream) : decode_rows<128, false>(c, in, rows, cut, stream);
 }
 
 size_t cache_decode_partial_bytes(int D) { return (size_t)2 * kDecodePieces * 16 * (D + 4) * sizeof(float); }

@@ -110,8 +110,10 @@ constexpr int kDecodePieces = 592;  // CTAs of the decode kernel: 4 on each of 1
 
 int launch_cache_append(const CacheArgs& c, const AppendIn& in, int D, bool q4, bool rotate, cudaStream_t stream);
 int launch_cache_read(const CacheArgs& c, int D, bool q4, void* k_out, void* v_out, cudaStream_t stream);
-// rows: query rows of a unit at most, as far as the caller knows (a choice of tile only)
-int launch_cache_decode(const CacheArgs& c, const AttnIn& in, int D, bool q4, int rows, cudaStream_t stream);
+// rows: query rows of a unit at most, as far as the caller knows (a choice of tile only); cut: units may be shared by
+// CTAs, and are joined in a second launch
+int launch_cache_decode(const CacheArgs& c, const AttnIn& in, int D, bool q4, int rows, bool cut,
+                        cudaStream_t stream);
 size_t cache_decode_partial_bytes(int D);
 
 constexpr int kChunkPieces = 148;  // CTAs of the chunk kernel: one on each SM

@@ -65,8 +65,20 @@ STEPS = [  # (lens, new tokens)
 @pytest.mark.parametrize("D,H,Hkv,S", [(128, 8, 2, 16), (64, 3, 3, 64)])
 @pytest.mark.parametrize("lens,news", STEPS)
 def test_few_new_tokens(bits, D, H, Hkv, S, lens, news):
+    # without and with the host's knowledge of the lengths: units are cut for long sequences, whole for short ones
     c = ref.Paged(lens, Hkv, D, S, bits, seed=len(lens) + lens[0])
-    check_attention(c, news, H, plain=all(n == 1 for n in news), max_new=max(news))
+    for max_len in (0, max(lens)):
+        check_attention(c, news, H, plain=all(n == 1 for n in news), max_new=max(news), max_len=max_len)
+
+
+@pytest.mark.parametrize("bits", [16, 4])
+def test_whole_units_of_uneven_batches(bits):
+    # more sequences than threads look at the lengths at once, rows in several blocks, empty sequences among them
+    lens = [(37 * i) % 300 for i in range(200)]
+    news = [min(n, 1 + i % 3) if i % 7 else 0 for i, n in enumerate(lens)]
+    c = ref.Paged(lens, 1, 64, 16, bits)
+    check_attention(c, news, 9, max_new=3, max_len=300)
+    check_attention(c, news, 9, max_new=3)
 
 
 @pytest.mark.parametrize("bits", [16, 4])
