@@ -23,6 +23,7 @@
 
 #include "s2_cache.cuh"
 #include "s2_kernels.h"
+#include "sm100_ptx.cuh"
 
 namespace s2 {
 
@@ -48,10 +49,11 @@ struct Token {
   bool store;  // and has a row in the cache
 };
 
+template <int N>
 __device__ __forceinline__ void find_tokens(const CacheArgs& c, int t0, Token* tok) {
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  if (warp < kTok) {
-    const int t = t0 + warp;
+  const int lane = threadIdx.x % 32;
+  for (int x = threadIdx.x / 32; x < N; x += kThreads / 32) {
+    const int t = t0 + x;
     Token r{0, 0, false, false};
     if (t < c.T) {
       const int b = seq_of_token(c, t, lane);
@@ -69,7 +71,7 @@ __device__ __forceinline__ void find_tokens(const CacheArgs& c, int t0, Token* t
         }
       }
     }
-    if (lane == 0) tok[warp] = r;
+    if (lane == 0) tok[x] = r;
   }
 }
 
@@ -96,28 +98,57 @@ __device__ __forceinline__ uint4 pack8(const float* x) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// min(rint(a / s), 15): by the reciprocal, whose product is within 1e-5 of the quotient, and by the division where
-// that could round the other way (or where s has no reciprocal).
-__device__ __forceinline__ uint32_t code_of(float a, float s, float inv) {
-  const float y = a * inv;
-  float n = rintf(y);
-  if (!(fabsf(fabsf(y - n) - 0.5f) > 1e-4f) || s < 1e-30f) n = rintf(__fdiv_rn(a, s));
-  return (uint32_t)fminf(n, 15.f);
+// Codes min(rint(a / s), 15) of a thread's 16 numbers a = x - min, as its 8 bytes.  By the reciprocal, added to
+// 1.5·2^23: the sum's low bits are the rounded quotient, with no conversion (those run at a quarter of the
+// rate), and eight sums' bits added up in their places, less eight times the constant's, are a word.  The product is
+// within 1e-5 of the quotient; where that could round the other way, or s has no reciprocal, the division decides.
+__device__ __forceinline__ uint2 codes_of(const Row& a, float s) {
+  constexpr float kMagic = 12582912.f;        // 0x4b400000
+  constexpr uint32_t kBits = 0x4b400000u * 0x11111111u;
+  const float inv = 1.0f / s;
+  uint32_t w[2];
+  float far = 0.f;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t sum = 0u - kBits;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float x = a.lo[4 * h + i], y = a.hi[4 * h + i];
+      const float lo = fmaf(x, inv, kMagic), hi = fmaf(y, inv, kMagic);
+      far = fmax3(far, fabsf(fmaf(x, inv, kMagic - lo)), fabsf(fmaf(y, inv, kMagic - hi)));
+      sum += __float_as_uint(lo) * (1u << (8 * i)) + __float_as_uint(hi) * (16u << (8 * i));
+    }
+    w[h] = sum;
+  }
+  if (!(far <= 0.4999f) || s < 1e-30f) {
+    w[0] = w[1] = 0u;
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t lo = (uint32_t)fminf(rintf(__fdiv_rn(a.lo[i], s)), 15.f);
+      const uint32_t hi = (uint32_t)fminf(rintf(__fdiv_rn(a.hi[i], s)), 15.f);
+      w[i / 4] |= (lo | (hi << 4)) << (8 * (i % 4));
+    }
+  }
+  return make_uint2(w[0], w[1]);
 }
+
+__device__ __forceinline__ __nv_bfloat162 as_pair(uint32_t x) { return *reinterpret_cast<__nv_bfloat162*>(&x); }
 
 // Packs a row held by LANES lanes (bf16 values) to 4 bits: this lane's 8 bytes and the row's (scale, min).
 // A row with a NaN or an infinity reads back as NaN.
 template <int LANES>
-__device__ __forceinline__ void pack_row(const Row& x, uint2& codes, uint32_t& pair) {
-  float mn = x.lo[0], mx = x.lo[0];
-  bool fine = true;
+__device__ __forceinline__ void pack_row(const uint4& lo, const uint4& hi, uint2& codes, uint32_t& pair) {
+  // extremes of pairs of numbers; 0 times a number that is none is none
+  const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+  const __nv_bfloat162 zero = as_pair(0u);
+  __nv_bfloat162 mn2 = as_pair(w[0]), mx2 = mn2, broken = zero;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    mn = fminf(mn, fminf(x.lo[i], x.hi[i]));
-    mx = fmaxf(mx, fmaxf(x.lo[i], x.hi[i]));
-    fine = fine && isfinite(x.lo[i]) && isfinite(x.hi[i]);
+    mn2 = __hmin2(mn2, as_pair(w[i]));
+    mx2 = __hmax2(mx2, as_pair(w[i]));
+    broken = __hfma2(as_pair(w[i]), zero, broken);
   }
-  int good = fine;
+  float mn = fminf(__low2float(mn2), __high2float(mn2)), mx = fmaxf(__low2float(mx2), __high2float(mx2));
+  int good = __low2float(broken) == 0.f && __high2float(broken) == 0.f;
 #pragma unroll
   for (int off = LANES / 2; off > 0; off >>= 1) {
     mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, off));
@@ -125,18 +156,20 @@ __device__ __forceinline__ void pack_row(const Row& x, uint2& codes, uint32_t& p
     good &= __shfl_xor_sync(0xffffffffu, good, off);
   }
   // the scale is rounded to bf16 (8 bits) before the codes are chosen, so the rounding moves the grid
-  // (by 2^-9 of it, at most 0.03 of a step at its end) and not the error of a value
-  __nv_bfloat16 sb = __float2bfloat16_rn((mx - mn) / 15.0f);
+  // (by 2^-8 of it at most, 0.06 of a step at its end) and not the error of a value
+  __nv_bfloat16 sb = __float2bfloat16_rn(__fdiv_rn(mx - mn, 15.0f));
   __nv_bfloat16 mb = __float2bfloat16_rn(mn);  // exact: the row is bf16
   const float s = __bfloat162float(sb);
-  uint32_t w[2] = {0u, 0u};
+  codes = make_uint2(0u, 0u);
   if (good && s > 0.f) {
-    const float inv = 1.0f / s;
+    Row x;
+    unpack8(lo, x.lo);
+    unpack8(hi, x.hi);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) w[i / 4] |= (code_of(x.lo[i] - mn, s, inv) | (code_of(x.hi[i] - mn, s, inv) << 4)) << (8 * (i % 4));
+    for (int i = 0; i < 8; ++i) x.lo[i] -= mn, x.hi[i] -= mn;
+    codes = codes_of(x, s);
   }
   if (!good) sb = mb = __float2bfloat16_rn(NAN);
-  codes = make_uint2(w[0], w[1]);
   pair = (uint32_t)__bfloat16_as_ushort(sb) | ((uint32_t)__bfloat16_as_ushort(mb) << 16);
 }
 
@@ -181,7 +214,7 @@ __global__ void __launch_bounds__(kThreads) s2_cache_append_kernel(const __grid_
     hi = *reinterpret_cast<const uint4*>(src + kHalf);
   };
   load(at);
-  find_tokens(c, t0, tok);
+  find_tokens<kTok>(c, t0, tok);
   __syncthreads();
   if constexpr (kRotate) {
     for (int i = threadIdx.x; i < kTok * kHalf; i += kThreads) {
@@ -231,11 +264,9 @@ __global__ void __launch_bounds__(kThreads) s2_cache_append_kernel(const __grid_
     }
     if constexpr (Q4) {
       if (!__any_sync(0xffffffffu, live && !is_q)) continue;
-      unpack8(out_lo, row.lo);  // the row as bf16 holds it
-      unpack8(out_hi, row.hi);
       uint2 codes;
       uint32_t pair;
-      pack_row<kLanes>(row, codes, pair);
+      pack_row<kLanes>(out_lo, out_hi, codes, pair);
       if (live && !is_q) {
         const size_t to = row_of(c, tok[now.x].page, h, tok[now.x].place);
         *reinterpret_cast<uint2*>(static_cast<uint8_t*>(is_v ? c.v : c.k) + to * kHalf + 8 * lane) = codes;
@@ -247,19 +278,19 @@ __global__ void __launch_bounds__(kThreads) s2_cache_append_kernel(const __grid_
 
 // The inverse: rows of the batch's tokens, k and v [T, Hkv, D] in bf16 (one rounding from 4 bits).
 // Tokens of no sequence, or with no row in the cache, are left as they are.
-template <int D, bool Q4>
+template <int D, bool Q4, int kTokens>
 __global__ void __launch_bounds__(kThreads) s2_cache_read_kernel(const __grid_constant__ CacheArgs c,
                                                                  __nv_bfloat16* __restrict__ k_out,
                                                                  __nv_bfloat16* __restrict__ v_out) {
   constexpr int kHalf = D / 2, kLanes = D / 16, kRows = kThreads / kLanes;
-  __shared__ Token tok[kTok];
-  const int t0 = blockIdx.x * kTok;
-  find_tokens(c, t0, tok);
+  __shared__ Token tok[kTokens];
+  const int t0 = blockIdx.x * kTokens;
+  find_tokens<kTokens>(c, t0, tok);
   __syncthreads();
   const int per_token = 2 * c.heads;
   const int lane = threadIdx.x % kLanes;
 #pragma unroll 2
-  for (int w = threadIdx.x / kLanes; w < kTok * per_token; w += kRows) {
+  for (int w = threadIdx.x / kLanes; w < kTokens * per_token; w += kRows) {
     const int x = w / per_token, r = w % per_token;
     if (!tok[x].store) continue;
     const bool is_v = r >= c.heads;
@@ -308,8 +339,13 @@ int launch_cache_append(const CacheArgs& c, const AppendIn& in, int D, bool q4, 
 
 template <int D, bool Q4>
 static int read_impl(const CacheArgs& c, void* k_out, void* v_out, cudaStream_t stream) {
-  s2_cache_read_kernel<D, Q4><<<(unsigned)((c.T + kTok - 1) / kTok), kThreads, 0, stream>>>(
-      c, static_cast<__nv_bfloat16*>(k_out), static_cast<__nv_bfloat16*>(v_out));
+  auto* k = static_cast<__nv_bfloat16*>(k_out);
+  auto* v = static_cast<__nv_bfloat16*>(v_out);
+  // finding the tokens takes as long as moving a few rows: many to a CTA, as long as that leaves CTAs for all SMs
+  if ((int64_t)c.T * c.heads >= 1 << 16)
+    s2_cache_read_kernel<D, Q4, 16><<<(unsigned)((c.T + 15) / 16), kThreads, 0, stream>>>(c, k, v);
+  else
+    s2_cache_read_kernel<D, Q4, kTok><<<(unsigned)((c.T + kTok - 1) / kTok), kThreads, 0, stream>>>(c, k, v);
   return (int)cudaGetLastError();
 }
 
