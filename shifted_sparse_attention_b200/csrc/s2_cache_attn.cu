@@ -587,6 +587,8 @@ __global__ void __launch_bounds__(kJoinThreads) s2_cache_join_kernel(const __gri
   long long seq_first;
   const Line line =
       find_piece<kJoinThreads>(c.B, in.pieces, in.min_piece, blockIdx.x + 1, sh.line, weight, b, seq_first);
+  // every CTA waits here, also one with nothing to do: the stream's next launch counts on this one's end alone
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const long long cut = line.piece * (blockIdx.x + 1);
   if (cut >= line.total) return;
   const Seq seq = load_seq(c, b);
@@ -596,7 +598,6 @@ __global__ void __launch_bounds__(kJoinThreads) s2_cache_join_kernel(const __gri
   if (cut <= first) return;  // the cut lies before the unit's first step
   const int p0 = (int)(first / line.piece), p1 = (int)(last / line.piece);  // pieces that hold its steps
   const int h = (int)(unit / blocks), rb = (int)(unit % blocks);
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   join_rows<D>(
       sh, min(kRows, seq.n * in.g - rb * kRows), (int)blockIdx.x - p0, p1 - p0, p0, p1,
       [&](int p, int row) {  // a piece's first partial unit is one that began before it

@@ -880,6 +880,8 @@ __global__ void __launch_bounds__(kJoinThreads) s2_cache_chunk_join_kernel(const
   long long start;
   const Line line =
       find_piece<kJoinThreads>(c.B, in.pieces, in.min_piece, blockIdx.x + 1, sh.line, weight_of, b, start);
+  // every CTA waits here, also one with nothing to do: the stream's next launch counts on this one's end alone
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const long long cut = line.piece * (blockIdx.x + 1);
   if (cut >= line.total) return;
   const Seq s = load_seq(c, b);
@@ -894,7 +896,6 @@ __global__ void __launch_bounds__(kJoinThreads) s2_cache_chunk_join_kernel(const
   const int q0 = p0 + (tile_at(tiles, line.piece * (p0 + 1) - begin, w) == 0);
   const int q1 = p1 - (tile_at(tiles, line.piece * p1 - begin, w) == tiles);
   if (q0 >= q1) return;  // one piece had all of the unit's tiles and wrote its rows
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   join_rows<D>(
       sh, min(s.n - j * u.d, u.d) * in.g, ((int)blockIdx.x - p0) * gridDim.y + blockIdx.y, (p1 - p0) * gridDim.y, q0,
       q1,

@@ -35,9 +35,9 @@ int take(const s2_cache* cache, const s2_cache_batch* batch, s2::CacheArgs* a) {
   if (batch->max_new < 0 || batch->max_new > batch->tokens)
     return report_error(S2_ERR_SHAPE, "max_new=%lld must be in [0, tokens=%lld]", (long long)batch->max_new,
                         (long long)batch->tokens);
-  if (batch->max_len < 0 || batch->table_width >= (int64_t(1) << 31) / S ||
+  if (batch->max_len < 0 || batch->table_width >= (int64_t(1) << 30) / S ||
       batch->max_len > batch->table_width * S)
-    return report_error(S2_ERR_SHAPE, "max_len=%lld must be in [0, table_width*page_size], which is below 2^31",
+    return report_error(S2_ERR_SHAPE, "max_len=%lld must be in [0, table_width*page_size], which is below 2^30",
                         (long long)batch->max_len);
   if (batch->seqs >= (int64_t(1) << 30) || batch->tokens >= (int64_t(1) << 30))
     return report_error(S2_ERR_UNSUPPORTED, "seqs and tokens must be below 2^30");

@@ -142,6 +142,23 @@ def test_hints_change_no_result_and_runs_repeat_bitwise(max_new):
     assert torch.equal(b, check_attention(c, news, 8, wide=True, max_new=200))
 
 
+def test_lengths_beyond_the_hints_are_served():
+    lens, news = [1500, 3, 700], [2, 1, 1]
+    c = ref.Paged(lens, 2, 128, 64, 16)
+    for hints in (dict(max_new=1, max_len=40), dict(max_new=2, max_len=600), dict(max_new=0, max_len=1)):
+        check_attention(c, news, 8, **hints)
+
+
+@pytest.mark.parametrize("bits", [16, 4])
+@pytest.mark.parametrize("wide", [False, True])
+def test_pages_shared_by_sequences(bits, wide):
+    # two conversations with one beginning: the same pages in both tables
+    c = ref.Paged([256, 300, 290], 2, 128, 32, bits)
+    c.table[1, :8] = c.table[0, :8]
+    c.table[2, :8] = c.table[0, :8]
+    check_attention(c, [1, 44, 34], 8, wide=wide, max_new=44)
+
+
 @pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("bits", [16, 4])
 def test_tokens_of_no_sequence_are_left_as_they_were(bits, wide):
@@ -414,6 +431,30 @@ def test_steps_captured_in_a_graph(bits):
         want = s2.cache_attention(twin, batch, s2.cache_append(twin, batch, k, v, q))
         assert torch.equal(o, want)
     assert torch.equal(cache.k.view(torch.uint8), twin.k.view(torch.uint8))
+    s2.check_status()
+
+
+@pytest.mark.parametrize("bits", [16, 4])
+def test_chunks_captured_in_a_graph(bits):
+    """A captured call of the kernel for many rows, replayed with other lengths, starts and pages."""
+    c = ref.Paged([700, 400], 2, 128, 64, bits, fill=0.0)
+    cache = on_gpu(c)
+    batch = batch_of(c, [200, 100], wide=True, max_new=200)
+    q = torch.randn(300, 8, 128, generator=torch.Generator().manual_seed(2)).bfloat16()
+    out, ws, dev = torch.empty(300, 8, 128).bfloat16().cuda(), s2.cache_attention_workspace(cache, batch, 8), q.cuda()
+    s2.cache_attention(cache, batch, dev, out=out, workspace=ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        s2.cache_attention(cache, batch, dev, out=out, workspace=ws)
+    table = batch.page_table.clone()
+    for lens, news in (([700, 400], [200, 100]), ([650, 77], [250, 50]), ([300, 0], [1, 299])):
+        batch.seq_lens.copy_(torch.tensor(lens)), batch.q_starts.copy_(starts_of(news))
+        batch.page_table.copy_(table)
+        graph.replay()
+        c.lens = lens
+        o, _, to, _ = ref.attention(c, q, starts_of(news))
+        assert ((out.double().cpu() - o).abs() <= to).all()
     s2.check_status()
 
 
