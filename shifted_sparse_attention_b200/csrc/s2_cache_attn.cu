@@ -2,11 +2,12 @@
 //
 // For new token t of sequence b at place p, head h of key/value head h / g:
 //     o = sum_{j <= p} softmax_j(q·k_j / sqrt(D)) v_j,   lse = ln sum exp.
-// From a 4-bit cache, with k_j = mk + sk·ck and codes centred, c' = c - 8
-// (exact in bf16):
-//     q·k_j       = sk (q·c'_j) + (mk + 8 sk) sum(q),
-//     sum p_j v_j = sum (p_j sv_j) c'_j + sum p_j (mv_j + 8 sv_j),
-// so the matrix products see whole numbers and nothing of a row is rounded.
+// From a 4-bit cache, with k_j = mk + sk·ck:
+//     q·k_j       = sk (q·(128 + ck_j)) + (mk - 128 sk) sum(q),
+//     sum p_j v_j = sum (p_j sv_j)(cv_j - 8) + sum p_j (mv_j + 8 sv_j),
+// so the matrix products see whole numbers, which bf16 holds as they are, and
+// nothing of a row is rounded (values centred: rounded weights then meet small
+// numbers).
 //
 // Bound: HBM (each row of the cache is read once, and serves the g·n rows of
 // queries that share it).  Everything else is arranged around keeping loads
@@ -27,9 +28,10 @@
 //   row; V's pairs along the keys are put together with byte permutes, the
 //   weights' with one 8x8 transposition (movmatrix).
 // - the running maximum moves only when a score passes it by more than 8 (a
-//   factor 256), which one vote per step tells; sums are in 32 bits, the
-//   weights are rounded to bf16 for the product (relative 2^-9 each, independent
-//   signs) and added up unrounded.
+//   factor 256), which one vote per step tells; sums are in 32 bits.  The
+//   weights are rounded to bf16 for the product (2^-8 of each at most); O is
+//   divided by the sum of the rounded ones where that is to be had (bf16 rows),
+//   so that it stays a mean of values, and lse comes from the unrounded sum.
 #include <climits>
 
 #include <cuda_bf16.h>
@@ -190,7 +192,7 @@ __host__ __device__ constexpr int ctas_per_sm() { return (NR == 2 ? 8 : Q4 ? 16 
 template <int D, int NR, int W>
 struct DecodeShared {
   long long line[W + 2];
-  float m[W][8 * NR], l[W][8 * NR];
+  float m[W][8 * NR], l[W][8 * NR], div[W][8 * NR];  // maximum, sum of weights, what O is divided by
   alignas(16) float o[W][8 * NR][D + 4];
 };
 
@@ -296,6 +298,7 @@ __global__ void __launch_bounds__(W * 32, ctas_per_sm<Q4, NR, W>())
 
     // ---------------------------------------------------------- keys
     float acc[NR][kTiles][4];
+    // maximum; sum of the weights; bf16 rows: of the weights as the product takes them, 4-bit rows: of weight·middle
     float m[NR][2], l[NR][2], vsum[NR][2];
 #pragma unroll
     for (int y = 0; y < NR; ++y) {
@@ -473,7 +476,12 @@ __global__ void __launch_bounds__(W * 32, ctas_per_sm<Q4, NR, W>())
                   w[e] *= pr.x;
                 }
               }
-              pf[y][t] = transpose8x8(pack_bf16(w[0], w[1]));
+              const uint32_t pk = pack_bf16(w[0], w[1]);
+              if constexpr (!Q4) {
+                vsum[y][0] += __uint_as_float(pk << 16);
+                vsum[y][1] += __uint_as_float(pk & 0xffff0000u);
+              }
+              pf[y][t] = transpose8x8(pk);
             }
           if constexpr (Q4) {
 #pragma unroll
@@ -531,12 +539,14 @@ __global__ void __launch_bounds__(W * 32, ctas_per_sm<Q4, NR, W>())
         const int row = y * 8 + 2 * cc + e;
 #pragma unroll
         for (int j = 0; j < kTiles; ++j) {
-          sh.o[warp][row][channel_of<D, Q4>(j, false, r)] = acc[y][j][e] + vsum[y][e];
-          sh.o[warp][row][channel_of<D, Q4>(j, true, r)] = acc[y][j][2 + e] + vsum[y][e];
+          const float add = Q4 ? vsum[y][e] : 0.f;
+          sh.o[warp][row][channel_of<D, Q4>(j, false, r)] = acc[y][j][e] + add;
+          sh.o[warp][row][channel_of<D, Q4>(j, true, r)] = acc[y][j][2 + e] + add;
         }
         if (r == 0) {
           sh.m[warp][row] = m[y][e];
           sh.l[warp][row] = l[y][e];
+          sh.div[warp][row] = Q4 ? l[y][e] : vsum[y][e];
         }
       }
     __syncthreads();
@@ -548,7 +558,7 @@ __global__ void __launch_bounds__(W * 32, ctas_per_sm<Q4, NR, W>())
       float mm = sh.m[0][row];
 #pragma unroll
       for (int w = 1; w < W; ++w) mm = fmaxf(mm, sh.m[w][row]);
-      float ll = 0.f;
+      float ll = 0.f, div = 0.f;
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < W; ++w) {
@@ -556,18 +566,19 @@ __global__ void __launch_bounds__(W * 32, ctas_per_sm<Q4, NR, W>())
         const float f = ex2(sh.m[w][row] - mm);
         const float4 v = *reinterpret_cast<const float4*>(&sh.o[w][row][d]);
         ll += sh.l[w][row] * f;
+        div += sh.div[w][row] * f;
         o.x += v.x * f, o.y += v.y * f, o.z += v.z * f, o.w += v.w * f;
       }
       if (whole) {
         const int at = rb * kRows + row;
         const size_t out = (size_t)(seq.first + at / in.g) * in.heads + h * in.g + at % in.g;
-        const float inv = ll > 0.f ? 1.f / ll : 0.f;
+        const float inv = ll > 0.f ? 1.f / div : 0.f;
         *reinterpret_cast<uint2*>(in.o + out * D + d) =
             make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
         if (in.lse && d == 0) in.lse[out] = ll > 0.f ? (mm + log2f(ll)) * 0.69314718055994531f : -INFINITY;
       } else {
         *reinterpret_cast<float4*>(part + row * kPartial<D> + d) = o;
-        if (d == 0) *reinterpret_cast<float2*>(part + row * kPartial<D> + D) = make_float2(mm, ll);
+        if (d == 0) *reinterpret_cast<float4*>(part + row * kPartial<D> + D) = make_float4(mm, ll, div, 0.f);
       }
     }
     __syncthreads();

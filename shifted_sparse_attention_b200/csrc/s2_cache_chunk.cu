@@ -838,7 +838,7 @@ do {                                                                            
           if (g.slot < 0) {
             if (in.lse) in.lse[out] = l > 0.f ? (m_used + log2f(l)) * 0.69314718055994531f : -INFINITY;
           } else {
-            *reinterpret_cast<float4*>(part + D) = make_float4(m_used, l, 0.f, 0.f);
+            *reinterpret_cast<float4*>(part + D) = make_float4(m_used, l, l, 0.f);
           }
         }
         tc_fence_before();  // O has been read: ordered before the next unit's first P_FULL arrival

@@ -2,8 +2,10 @@
 // that several CTAs computed (s2_cache_attn.cu, s2_cache_chunk.cu).
 //
 // A piece leaves for each row O (D floats, not divided), then its maximum
-// score and sum of weights; in the order of the pieces
-//     m = max m_p,  o = sum 2^(m_p - m) O_p / sum 2^(m_p - m) l_p.
+// score, the sum of its weights and what O is to be divided by; in the order of
+// the pieces
+//     m = max m_p,  o = sum 2^(m_p - m) O_p / sum 2^(m_p - m) d_p,
+// and lse from the sum of weights.
 // What bounds it is the latency of reading them, so all of a warp's loads are
 // asked for before the first is used: with up to 8 pieces a warp takes a row,
 // with more a CTA does, its warps sharing the pieces.
@@ -25,31 +27,31 @@ constexpr int kPartial = D + 4;
 template <int D>
 struct JoinShared {
   long long line[kJoinThreads / 32 + 2];
-  float m[kJoinThreads / 32], l[kJoinThreads / 32];
+  float m[kJoinThreads / 32], l[kJoinThreads / 32], d[kJoinThreads / 32];
   alignas(16) float o[kJoinThreads / 32][D];
 };
 
 // Sum of pieces p, p + by, .. <= p1 of one row: a lane holds channels [lane·D/32, ..).
 template <int D, typename Part>
 __device__ __forceinline__ void join_pieces(int p, int by, int p1, int row, Part part, float& m, float& l,
-                                            float (&o)[D / 32]) {
+                                            float& d, float (&o)[D / 32]) {
   constexpr int kV = D / 32;
   const int lane = threadIdx.x % 32;
   m = -INFINITY;
-  l = 0.f;
+  l = d = 0.f;
 #pragma unroll
   for (int z = 0; z < kV; ++z) o[z] = 0.f;
   for (; p <= p1; p += kJoinBatch * by) {
-    float2 ml[kJoinBatch];
+    float4 ml[kJoinBatch];
     float v[kJoinBatch][kV];
 #pragma unroll
     for (int i = 0; i < kJoinBatch; ++i) {
-      ml[i] = make_float2(-INFINITY, 0.f);
+      ml[i] = make_float4(-INFINITY, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int z = 0; z < kV; ++z) v[i][z] = 0.f;
       if (p + i * by <= p1) {
         const float* from = part(p + i * by, row);
-        ml[i] = *reinterpret_cast<const float2*>(from + D);
+        ml[i] = *reinterpret_cast<const float4*>(from + D);
         if constexpr (kV == 4) {
           const float4 t = *reinterpret_cast<const float4*>(from + 4 * lane);
           v[i][0] = t.x, v[i][1] = t.y, v[i][2] = t.z, v[i][3] = t.w;
@@ -65,12 +67,14 @@ __device__ __forceinline__ void join_pieces(int p, int by, int p1, int row, Part
     if (top == -INFINITY) continue;
     const float f = ex2(m - top);
     l *= f;
+    d *= f;
 #pragma unroll
     for (int z = 0; z < kV; ++z) o[z] *= f;
 #pragma unroll
     for (int i = 0; i < kJoinBatch; ++i) {
       const float g = ex2(ml[i].x - top);
       l = fmaf(ml[i].y, g, l);
+      d = fmaf(ml[i].z, g, d);
 #pragma unroll
       for (int z = 0; z < kV; ++z) o[z] = fmaf(v[i][z], g, o[z]);
     }
@@ -88,29 +92,30 @@ __device__ __forceinline__ void join_rows(JoinShared<D>& sh, int rows, int nth, 
   const bool narrow = p1 - p0 < kJoinBatch;
   const int first = narrow ? nth * kW + warp : nth, by = narrow ? helpers * kW : helpers;
   for (int row = first; row < rows; row += by) {
-    float m, l, o[kV];
-    join_pieces<D>(narrow ? p0 : p0 + warp, narrow ? 1 : kW, p1, row, part, m, l, o);
+    float m, l, div, o[kV];
+    join_pieces<D>(narrow ? p0 : p0 + warp, narrow ? 1 : kW, p1, row, part, m, l, div, o);
     if (!narrow) {
       __syncthreads();
-      if (lane == 0) sh.m[warp] = m, sh.l[warp] = l;
+      if (lane == 0) sh.m[warp] = m, sh.l[warp] = l, sh.d[warp] = div;
 #pragma unroll
       for (int z = 0; z < kV; ++z) sh.o[warp][kV * lane + z] = o[z];
       __syncthreads();
       if (warp != 0) continue;
 #pragma unroll
       for (int w = 1; w < kW; ++w) m = fmaxf(m, sh.m[w]);
-      l = 0.f;
+      l = div = 0.f;
 #pragma unroll
       for (int z = 0; z < kV; ++z) o[z] = 0.f;
 #pragma unroll
       for (int w = 0; w < kW; ++w) {
         const float f = m == -INFINITY ? 0.f : ex2(sh.m[w] - m);
         l = fmaf(sh.l[w], f, l);
+        div = fmaf(sh.d[w], f, div);
 #pragma unroll
         for (int z = 0; z < kV; ++z) o[z] = fmaf(sh.o[w][kV * lane + z], f, o[z]);
       }
     }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const float inv = l > 0.f ? 1.f / div : 0.f;
     const size_t at = out(row);
     uint32_t* dst = reinterpret_cast<uint32_t*>(o_all + at * D) + lane * (kV / 2);
     if constexpr (kV == 4)

@@ -98,8 +98,9 @@ def attention(cache, q, starts):
     Scores: products of bf16 values are exact in 32 bits; a sum of D of them and the scaling are off by at most (D + 8)
     roundings of the terms' absolute sum.  The terms of 4-bit rows are q·scale·(128 + code) and q·(min - 128 scale): bf16
     holds 128 + code as it is, and the two sums are taken one from the other.  Weights: twice that, relatively, and
-    2^-21 of the exponential.  o: each weight is rounded to bf16 before the product (U of its term), the sums over n
-    keys by n F, and the result once to bf16.  lse: the scores' error, the sum's, and a few roundings of itself."""
+    2^-21 of the exponential.  o: each weight is rounded to bf16 before the product, and from bf16 rows the sum of the
+    rounded ones may be what divides (2 U of a term; from 4 bits U), the sums over n keys are off by n F, and the
+    result is rounded once to bf16.  lse: the scores' error, the sum's, and a few roundings of itself."""
     T, H, D = q.shape
     g = H // cache.heads
     o, lse = torch.zeros(T, H, D, dtype=torch.float64), torch.full((T, H), -math.inf, dtype=torch.float64)
@@ -130,6 +131,6 @@ def attention(cache, q, starts):
                 out, size = p @ v, p @ va
                 rows = torch.arange(t0, t1)[some]
                 o[rows, y] = out
-                to[rows, y] = U * out.abs() + (U + rel[:, None]) * (1 + U) * size + rel[:, None] * (p @ v.abs())
+                to[rows, y] = U * out.abs() + ((2 * U if cache.bits == 16 else U) + rel[:, None]) * (1 + U) * size + rel[:, None] * (p @ v.abs())
                 tl[rows, y] = ds + 2.0 ** -21 + n * F + 4 * F * lse[rows, y].abs()
     return o, lse, to, tl
