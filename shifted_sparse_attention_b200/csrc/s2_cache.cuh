@@ -87,6 +87,11 @@ struct Line {
   long long total, piece;
 };
 
+// a / b of numbers >= 0: in 32 bits where they fit, which is a fraction of the time.
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
 // Shared memory of the two calls below: kThreads / 32 + 2 values.
 template <int kThreads, typename Weight>
 __device__ __forceinline__ Line make_line(int B, int pieces, long long min_piece, long long* sh, Weight weight) {
@@ -102,7 +107,7 @@ __device__ __forceinline__ Line make_line(int B, int pieces, long long min_piece
   l.total = 0;
 #pragma unroll
   for (int w = 0; w < kW; ++w) l.total += sh[w];
-  l.piece = (l.total + pieces - 1) / pieces;
+  l.piece = quotient(l.total + pieces - 1, pieces);
   if (l.piece < min_piece) l.piece = min_piece;
   return l;
 }
@@ -181,7 +186,7 @@ __device__ __forceinline__ Line find_piece(int B, int pieces, long long min_piec
     if (w < warp) end += sh[w];
     l.total += sh[w];
   }
-  l.piece = (l.total + pieces - 1) / pieces;
+  l.piece = quotient(l.total + pieces - 1, pieces);
   if (l.piece < min_piece) l.piece = min_piece;
   const long long x = l.piece * index;
   if (x < end && x >= end - mine) {

@@ -16,7 +16,7 @@
 //   are cut into steps of kStep keys.  All units' steps form one line, cut
 //   into equal pieces, one per CTA, so sequences of any lengths load all SMs
 //   alike; a unit cut by a border leaves partial sums (max, sum, O) that
-//   s2_cache_join adds up in a fixed order.
+//   a second launch adds up in a fixed order.
 // - a warp takes every fourth step of its CTA's piece by itself: loads go from
 //   global memory straight to the registers that mma.sync reads as its A
 //   operand (S^T = K Q^T and O^T = V^T P^T, so keys fill the 16-row side and
@@ -192,6 +192,7 @@ __host__ __device__ constexpr int ctas_per_sm() { return (NR == 2 ? 8 : Q4 ? 16 
 template <int D, int NR, int W>
 struct DecodeShared {
   long long line[W + 2];
+  long long x0, x1;  // the CTA's piece [x0, x1) of the line: here and not in registers, which the keys need
   float m[W][8 * NR], l[W][8 * NR], div[W][8 * NR];  // maximum, sum of weights, what O is divided by
   alignas(16) float o[W][8 * NR][D + 4];
 };
@@ -217,17 +218,20 @@ __global__ void __launch_bounds__(W * 32, ctas_per_sm<Q4, NR, W>())
   long long seq_first;
   const Line line = find_piece<kThreads>(c.B, cut ? in.pieces : INT_MAX, in.min_piece, blockIdx.x, sh.line, weight, b,
                                          seq_first);
-  const long long x0 = line.piece * blockIdx.x;
-  if (x0 >= line.total) return;
-  const long long x1 = min(x0 + line.piece, line.total);
+  if (line.piece * blockIdx.x >= line.total) return;
+  if (threadIdx.x == 0) {
+    sh.x0 = line.piece * blockIdx.x;
+    sh.x1 = min(line.piece * (blockIdx.x + 1), line.total);
+  }
+  __syncthreads();
   // a lane's place in a block of 16 rows
   const uint8_t* const k_base = static_cast<const uint8_t*>(c.k) + r * kRowBytes + (Q4 ? (D / 8) : 16) * cc;
   const uint8_t* const v_base = static_cast<const uint8_t*>(c.v) + 2 * cc * kRowBytes + (Q4 ? (D / 16) : 16) * r;
   const uint8_t* const ks_base = static_cast<const uint8_t*>(c.k_scale) + 4 * r;
   const uint8_t* const vs_base = static_cast<const uint8_t*>(c.v_scale) + 4 * r;
 
-  long long x = x0;
-  while (x < x1) {
+  long long x = sh.x0;
+  while (x < sh.x1) {
     Seq seq = load_seq(c, b);
     const int blocks = row_blocks<NR>(seq.n, in.g);
     const int steps = steps_of(seq.len, kStep);
@@ -237,14 +241,14 @@ __global__ void __launch_bounds__(W * 32, ctas_per_sm<Q4, NR, W>())
       ++b;
       continue;
     }
-    const long long unit = (x - seq_first) / span;
+    const long long unit = quotient(x - seq_first, span);
     const long long unit_first = seq_first + unit * span + head;  // of its steps
-    const int h = (int)(unit / blocks), rb = (int)(unit % blocks);
+    const int h = (int)quotient(unit, blocks), rb = (int)(unit - (long long)h * blocks);
     const int k0 = (int)max(0LL, x - unit_first);
-    const int k1 = cut ? (int)min((long long)steps, x1 - unit_first) : steps;
+    const int k1 = cut ? (int)min((long long)steps, sh.x1 - unit_first) : steps;
     x = unit_first + (cut ? steps : 1);
     if (k1 <= k0) continue;
-    const bool whole = k0 == 0 && k1 == steps;
+    const int slot = k0 == 0 && k1 == steps ? -1 : 2 * (int)blockIdx.x + (unit_first < sh.x0 ? 0 : 1);  // -1: whole
 
     // ---------------------------------------------------------- query rows
     // B operand of S^T: lane (r, cc) holds row r's channels as load_keys orders them
@@ -552,7 +556,7 @@ __global__ void __launch_bounds__(W * 32, ctas_per_sm<Q4, NR, W>())
     __syncthreads();
     // four channels of a row a thread; rows of no token are left out
     const int rows_here = min(kRows, seq.n * in.g - rb * kRows);
-    float* part = in.partial + (size_t)(2 * blockIdx.x + (unit_first < x0 ? 0 : 1)) * kRows * kPartial<D>;
+    float* part = in.partial + (size_t)slot * kRows * kPartial<D>;
     for (int i = threadIdx.x; i < rows_here * (D / 4); i += kThreads) {
       const int row = i / (D / 4), d = 4 * (i % (D / 4));
       float mm = sh.m[0][row];
@@ -569,7 +573,7 @@ __global__ void __launch_bounds__(W * 32, ctas_per_sm<Q4, NR, W>())
         div += sh.div[w][row] * f;
         o.x += v.x * f, o.y += v.y * f, o.z += v.z * f, o.w += v.w * f;
       }
-      if (whole) {
+      if (slot < 0) {
         const int at = rb * kRows + row;
         const size_t out = (size_t)(seq.first + at / in.g) * in.heads + h * in.g + at % in.g;
         const float inv = ll > 0.f ? 1.f / div : 0.f;
@@ -586,39 +590,43 @@ __global__ void __launch_bounds__(W * 32, ctas_per_sm<Q4, NR, W>())
 }
 
 // Joins the partial sums of units that the line's cuts run through.  CTA i
-// stands for cut i + 1; the CTAs of one unit's cuts share its rows out.
+// stands for cut i + 1; the CTAs of one unit's cuts share its rows out.  They
+// find the unit by themselves, while the sums are still being made.
 template <int D, bool Q4, int NR, int W>
 __global__ void __launch_bounds__(kJoinThreads) s2_cache_join_kernel(const __grid_constant__ CacheArgs c,
                                                                      const __grid_constant__ AttnIn in) {
   constexpr int kStep = 16 * step_blocks<Q4>();
   constexpr int kRows = 8 * NR;
+  __shared__ long long line_sh[kJoinThreads / 32 + 2];
   __shared__ JoinShared<D> sh;
   auto weight = [&](int i) { return seq_steps<NR, W>(c, in, i, kStep, true); };
   int b;
   long long seq_first;
   const Line line =
-      find_piece<kJoinThreads>(c.B, in.pieces, in.min_piece, blockIdx.x + 1, sh.line, weight, b, seq_first);
-  // every CTA waits here, also one with nothing to do: the stream's next launch counts on this one's end alone
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+      find_piece<kJoinThreads>(c.B, in.pieces, in.min_piece, blockIdx.x + 1, line_sh, weight, b, seq_first);
   const long long cut = line.piece * (blockIdx.x + 1);
-  if (cut >= line.total) return;
-  const Seq seq = load_seq(c, b);
-  const int steps = steps_of(seq.len, kStep), blocks = row_blocks<NR>(seq.n, in.g), span = steps + unit_steps<W>();
-  const long long unit = (cut - seq_first) / span;
-  const long long first = seq_first + unit * span + unit_steps<W>(), last = first + steps - 1;  // of its steps
-  if (cut <= first) return;  // the cut lies before the unit's first step
-  const int p0 = (int)(first / line.piece), p1 = (int)(last / line.piece);  // pieces that hold its steps
-  const int h = (int)(unit / blocks), rb = (int)(unit % blocks);
-  join_rows<D>(
-      sh, min(kRows, seq.n * in.g - rb * kRows), (int)blockIdx.x - p0, p1 - p0, p0, p1,
-      [&](int p, int row) {  // a piece's first partial unit is one that began before it
-        return in.partial + ((size_t)(2 * p + (first < line.piece * p ? 0 : 1)) * kRows + row) * kPartial<D>;
-      },
-      [&](int row) {
-        const int at = rb * kRows + row;
-        return (size_t)(seq.first + at / in.g) * in.heads + h * in.g + at % in.g;
-      },
-      in.o, in.lse);
+  JoinCut u;
+  u.rows = 0;
+  if (cut < line.total) {
+    const Seq seq = load_seq(c, b);
+    const int steps = steps_of(seq.len, kStep), blocks = row_blocks<NR>(seq.n, in.g), span = steps + unit_steps<W>();
+    const long long unit = quotient(cut - seq_first, span);
+    const long long first = seq_first + unit * span + unit_steps<W>();  // of its steps
+    if (cut > first) {  // and not before the unit's first step
+      const int h = (int)quotient(unit, blocks), rb = (int)(unit - (long long)h * blocks);
+      u.rows = min(kRows, seq.n * in.g - rb * kRows);
+      u.begin = u.p0 = (int)quotient(first, line.piece);
+      u.p1 = (int)quotient(first + steps - 1, line.piece);
+      u.nth = (int)blockIdx.x - u.p0;
+      u.helpers = u.p1 - u.p0;
+      u.tok = seq.first;
+      u.row0 = rb * kRows;
+      u.head = h * in.g;
+    }
+  }
+  // every CTA waits, also one with nothing to do: the stream's next launch counts on this one's end alone
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  join_rows<D>(sh, u, in.partial, kRows, in.g, in.heads, [](int i) { return i; }, in.o, in.lse);
 }
 
 template <int D, bool Q4, int NR, int W>

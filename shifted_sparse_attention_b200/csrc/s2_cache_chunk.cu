@@ -84,6 +84,7 @@ struct Seg {
 struct Walk {
   long long at, x0, x1;  // of the piece [x0, x1)
   long long start;       // where sequence b begins
+  long long piece;
   int b, h, j;
 };
 
@@ -106,22 +107,28 @@ struct Layout {
   static constexpr int kAlloc = kBytes + 1024;
 };
 
-// Sequence b cut into units: pair j holds new tokens [j·d, (j + 1)·d), d = 2·(128 / g).
-// Their weights grow by d, so sums have a closed form.
+// Sequence b cut into units: pair j holds new tokens [j·d, (j + 1)·d), d = 2·(128 / g), which see up to
+// first + (j + 1)·d keys.  A unit weighs as many keys and kUnitKeys; sums of weights have a closed form.  (That
+// the weights are exact, and a piece at least 384, leaves a key tile in every piece between a unit's first and last.)
 struct Units {
-  long long past;  // keys before the new tokens
+  long long first;  // place of the first new token; negative where a sequence is shorter than its new tokens
   int n, d, pairs;
+  int blind;        // pairs that see no key
   __device__ __forceinline__ Units(const Seq& s, int per_tile) {
     n = s.n;
     d = 2 * per_tile;
     pairs = (n + d - 1) / d;
-    past = max(0, s.len - s.n);
+    first = (long long)s.len - s.n;
+    blind = first < 0 ? (s.n - s.len) / d : 0;
   }
-  __device__ __forceinline__ long long weight(int j) const { return past + (long long)(j + 1) * d + kUnitKeys; }
+  __device__ __forceinline__ long long weight(int j) const {
+    return kUnitKeys + (j == pairs - 1 ? first + n : j < blind ? 0 : first + (long long)(j + 1) * d);
+  }
   __device__ __forceinline__ long long before(int j) const {
-    return j * (past + kUnitKeys) + (long long)d * j * (j + 1) / 2;
+    const long long see = j > blind ? j - blind : 0;  // pairs before j that see keys: blind .. j - 1
+    return j * kUnitKeys + see * first + (long long)d * (see * (blind + 1) + see * (see - 1) / 2);
   }
-  __device__ __forceinline__ long long head() const { return before(pairs); }
+  __device__ __forceinline__ long long head() const { return before(pairs - 1) + kUnitKeys + first + n; }
   // The pair that holds point r of a head's units.
   __device__ __forceinline__ int find(long long r) const {
     int lo = 0, hi = pairs - 1;
@@ -148,39 +155,56 @@ __device__ __forceinline__ int tile_at(int tiles, long long w, long long weight)
   return w >= weight ? tiles : min(tiles, __double2int_rd(__ddiv_rn((double)w * tiles, (double)weight)));
 }
 
-// The next segments of a CTA's piece (one thread); returns their number.
-__device__ __noinline__ int walk_on(Walk& w, const CacheArgs& c, int per_tile, Seg* segs, int most) {
+// The next segments of a CTA's piece (one thread); returns their number.  What the piece's end cuts goes to `cut`.
+__device__ __noinline__ int walk_on(Walk& w, const CacheArgs& c, int g_heads, int per_tile, Seg* segs, int most,
+                                    JoinCut* cut) {
   int k = 0;
   if (w.at >= w.x1) return 0;
   Seq s = load_seq(c, w.b);
   while (k < most && w.at < w.x1) {
-    const Units u(s, per_tile);
-    if (w.j >= u.pairs) {
+    const Units units(s, per_tile);
+    const int u_d = units.d;
+    if (w.j >= units.pairs) {
       w.j = 0;
       ++w.h;
     }
     if (s.n == 0 || w.h >= c.heads) {
-      if (s.n > 0) w.start += u.head() * c.heads;
+      if (s.n > 0) w.start += units.head() * c.heads;
       w.h = w.j = 0;
       s = load_seq(c, ++w.b);
       continue;
     }
-    const long long weight = u.weight(w.j);
-    const long long begin = w.start + w.h * u.head() + u.before(w.j), end = begin + weight;
-    const int tiles = pair_tiles(s, u, w.j);
+    const long long weight = units.weight(w.j);
+    const long long begin = w.start + w.h * units.head() + units.before(w.j), end = begin + weight;
+    const int tiles = pair_tiles(s, units, w.j);
     const int ta = tile_at(tiles, max(w.at, begin) - begin, weight);
     const int tb = tile_at(tiles, min(w.x1, end) - begin, weight);
     if (tiles ? tb > ta : w.at <= begin) {
       Seg& g = segs[k++];
       g.b = w.b;
       g.h = w.h;
-      g.tok = s.first + w.j * u.d;
-      g.left = s.n - w.j * u.d;
-      g.place = s.len - s.n + w.j * u.d;
+      g.tok = s.first + w.j * u_d;
+      g.left = s.n - w.j * u_d;
+      g.place = s.len - s.n + w.j * u_d;
       g.len = s.len;
       g.t0 = ta;
       g.t1 = tb;
-      g.slot = (ta == 0 && tb == tiles) ? -1 : 2 * (int)blockIdx.x + (begin <= w.x0 ? 0 : 1);
+      g.slot = (ta == 0 && tb == tiles) ? -1 : 2 * (int)blockIdx.x + (begin < w.x0 ? 0 : 1);
+    }
+    if (end > w.x1 && tiles > 0) {
+      const int p0 = (int)quotient(begin, w.piece), p1 = (int)quotient(end - 1, w.piece);
+      JoinCut u;
+      u.rows = min(s.n - w.j * u_d, u_d) * g_heads;
+      u.nth = (int)blockIdx.x - p0;
+      u.helpers = p1 - p0;
+      u.begin = p0;
+      // pieces between hold tiles; the first and the last may hold none
+      u.p0 = p0 + (tile_at(tiles, w.piece * (p0 + 1) - begin, weight) == 0);
+      u.p1 = p1 - (tile_at(tiles, w.piece * p1 - begin, weight) == tiles);
+      u.tok = s.first + w.j * u_d;
+      u.row0 = 0;
+      u.head = w.h * g_heads;
+      if (u.p0 < u.p1) *cut = u;  // else one piece has all of the unit's tiles, and writes its rows
     }
     w.at = min(w.x1, end);
     ++w.j;
@@ -221,6 +245,11 @@ __global__ void __launch_bounds__(chunk::threads<Q4>(), 1)
   constexpr int kList = Q4 ? kSegs : 16;
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (threadIdx.x == 256) {  // the TMA warp
+    prefetch_tmap(&tmQ);
+    prefetch_tmap(&tmK);
+    prefetch_tmap(&tmV);
+  }
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sb = smem_u32(smem);
@@ -290,11 +319,13 @@ __global__ void __launch_bounds__(chunk::threads<Q4>(), 1)
     walk->x0 = x0;
     walk->x1 = max(x0, x1);
     walk->start = b_start;
+    walk->piece = line.piece;
+    static_cast<JoinCut*>(in.cuts)[blockIdx.x].rows = 0;
     if (x0 < x1) {
       const Units u(load_seq(c, b_first), per_tile);
       walk->b = b_first;
-      walk->h = (int)((x0 - b_start) / u.head());
-      walk->j = u.find((x0 - b_start) % u.head());
+      walk->h = (int)quotient(x0 - b_start, u.head());
+      walk->j = u.find(x0 - b_start - walk->h * u.head());
     }
   }
 
@@ -303,7 +334,8 @@ __global__ void __launch_bounds__(chunk::threads<Q4>(), 1)
   bool ok = true;
   auto next_list = [&]() -> int {
     __syncthreads();  // everyone is done with the last list
-    if (threadIdx.x == 0) *count = *abort_flag ? 0 : walk_on(*walk, c, per_tile, segs, kList);
+    if (threadIdx.x == 0) *count = *abort_flag ? 0 : walk_on(*walk, c, in.g, per_tile, segs, kList,
+                                                            static_cast<JoinCut*>(in.cuts) + blockIdx.x);
     __syncthreads();
     return *count;
   };
@@ -865,45 +897,21 @@ do {                                                                            
 
 // Joins the partial sums of units that the line's cuts run through: blocks
 // (i, y) stand for cut i + 1, and share the unit's rows with the blocks of its
-// other cuts.
+// other cuts.  What there is to join they read from the pieces' notes: finding
+// it again took each of the many blocks longer than the joining.
 template <int D>
-__global__ void __launch_bounds__(kJoinThreads) s2_cache_chunk_join_kernel(const __grid_constant__ CacheArgs c,
-                                                                           const __grid_constant__ AttnIn in) {
+__global__ void __launch_bounds__(kJoinThreads) s2_cache_chunk_join_kernel(const __grid_constant__ AttnIn in) {
   using namespace chunk;
   __shared__ JoinShared<D> sh;
   const int per_tile = kT / in.g;
-  auto weight_of = [&](int b) -> long long {
-    const Seq s = load_seq(c, b);
-    return s.n > 0 ? Units(s, per_tile).head() * c.heads : 0;
-  };
-  int b;
-  long long start;
-  const Line line =
-      find_piece<kJoinThreads>(c.B, in.pieces, in.min_piece, blockIdx.x + 1, sh.line, weight_of, b, start);
-  // every CTA waits here, also one with nothing to do: the stream's next launch counts on this one's end alone
+  // every CTA waits, also one with nothing to do: the stream's next launch counts on this one's end alone
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const long long cut = line.piece * (blockIdx.x + 1);
-  if (cut >= line.total) return;
-  const Seq s = load_seq(c, b);
-  const Units u(s, per_tile);
-  const int h = (int)((cut - start) / u.head());
-  const int j = u.find((cut - start) % u.head());
-  const long long begin = start + h * u.head() + u.before(j), w = u.weight(j);
-  if (begin == cut) return;
-  const int tiles = pair_tiles(s, u, j);
-  const int p0 = (int)(begin / line.piece), p1 = (int)((begin + w - 1) / line.piece);
-  // pieces between hold tiles (a piece is many tiles long); the first and the last may hold none
-  const int q0 = p0 + (tile_at(tiles, line.piece * (p0 + 1) - begin, w) == 0);
-  const int q1 = p1 - (tile_at(tiles, line.piece * p1 - begin, w) == tiles);
-  if (q0 >= q1) return;  // one piece had all of the unit's tiles and wrote its rows
-  join_rows<D>(
-      sh, min(s.n - j * u.d, u.d) * in.g, ((int)blockIdx.x - p0) * gridDim.y + blockIdx.y, (p1 - p0) * gridDim.y, q0,
-      q1,
-      [&](int p, int i) {
-        const int tok = i / in.g, row = (tok / per_tile) * kT + (tok % per_tile) * in.g + i % in.g;
-        return in.partial + ((size_t)(2 * p + (begin <= line.piece * p ? 0 : 1)) * 2 * kT + row) * kPartial<D>;
-      },
-      [&](int i) { return (size_t)(s.first + j * u.d + i / in.g) * in.heads + h * in.g + i % in.g; }, in.o, in.lse);
+  join_rows<D>(sh, static_cast<const JoinCut*>(in.cuts)[blockIdx.x], in.partial, 2 * kT, in.g, in.heads,
+               [&](int i) {
+                 const int tok = i / in.g;
+                 return (tok / per_tile) * kT + (tok % per_tile) * in.g + i % in.g;
+               },
+               in.o, in.lse);
 }
 
 template <int D, bool Q4>
@@ -926,7 +934,7 @@ static int chunk_impl(const CUtensorMap* tq, const CUtensorMap* tk, const CUtens
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return (int)cudaLaunchKernelEx(&cfg, s2_cache_chunk_join_kernel<D>, c, in);
+  return (int)cudaLaunchKernelEx(&cfg, s2_cache_chunk_join_kernel<D>, in);
 }
 
 int launch_cache_chunk(const CUtensorMap* tq, const CUtensorMap* tk, const CUtensorMap* tv, const CacheArgs& c,
@@ -936,8 +944,10 @@ int launch_cache_chunk(const CUtensorMap* tq, const CUtensorMap* tk, const CUten
   return q4 ? chunk_impl<128, true>(tq, tk, tv, c, in, stream) : chunk_impl<128, false>(tq, tk, tv, c, in, stream);
 }
 
+static_assert(kChunkPieces * sizeof(JoinCut) <= kCutBytes, "room for the notes");
+
 size_t cache_chunk_partial_bytes(int D) {
-  return (size_t)2 * kChunkPieces * 2 * chunk::kT * (D + 4) * sizeof(float);
+  return kCutBytes + (size_t)2 * kChunkPieces * 2 * chunk::kT * (D + 4) * sizeof(float);
 }
 
 }  // namespace s2

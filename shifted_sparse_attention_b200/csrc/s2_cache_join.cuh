@@ -24,9 +24,20 @@ constexpr int kJoinBatch = 8;  // pieces that a warp asks for at once
 template <int D>
 constexpr int kPartial = D + 4;
 
+// A unit that the end of a piece cuts; rows = 0: it cuts none.
+struct alignas(16) JoinCut {
+  int rows;          // query rows of the unit
+  int nth, helpers;  // which of the unit's cuts this is, and how many there are
+  int begin;         // piece in which the unit begins: its sums are in the piece's second slot, the others' in the first
+  int p0, p1;        // pieces that hold sums
+  int tok, row0;     // row i is query row row0 + i of the heads from `head` on, from token tok on
+  int head;
+  int pad[3];
+};
+constexpr size_t kCutBytes = 8192;  // of a workspace, before the sums, where pieces note what they cut
+
 template <int D>
 struct JoinShared {
-  long long line[kJoinThreads / 32 + 2];
   float m[kJoinThreads / 32], l[kJoinThreads / 32], d[kJoinThreads / 32];
   alignas(16) float o[kJoinThreads / 32][D];
 };
@@ -82,18 +93,24 @@ __device__ __forceinline__ void join_pieces(int p, int by, int p1, int row, Part
   }
 }
 
-// Rows of a unit whose pieces are p0..p1, shared out over `helpers` CTAs (this one is `nth`).
-// part(p, row): a row's partial sums of piece p; out(row): its number in o and lse.
-template <int D, typename Part, typename Out>
-__device__ __forceinline__ void join_rows(JoinShared<D>& sh, int rows, int nth, int helpers, int p0, int p1, Part part,
-                                          Out out, __nv_bfloat16* o_all, float* lse) {
+// Rows of a cut unit, shared out over the CTAs of its cuts (gridDim.y for each).  row_of_slot(i): place of row i
+// among the rows of a slot.
+template <int D, typename RowOfSlot>
+__device__ __forceinline__ void join_rows(JoinShared<D>& sh, const JoinCut u, const float* partial, int slot_rows,
+                                          int g, int heads, RowOfSlot row_of_slot, __nv_bfloat16* o_all, float* lse) {
   constexpr int kW = kJoinThreads / 32, kV = D / 32;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const bool narrow = p1 - p0 < kJoinBatch;
+  if (u.rows == 0) return;
+  const int nth = u.nth * gridDim.y + blockIdx.y, helpers = u.helpers * gridDim.y;
+  const bool narrow = u.p1 - u.p0 < kJoinBatch;
   const int first = narrow ? nth * kW + warp : nth, by = narrow ? helpers * kW : helpers;
-  for (int row = first; row < rows; row += by) {
+  auto part = [&](int p, int row) {
+    return partial + ((size_t)(2 * p + (p == u.begin)) * slot_rows + row) * kPartial<D>;
+  };
+  for (int i = first; i < u.rows; i += by) {
+    const int row = row_of_slot(i);
     float m, l, div, o[kV];
-    join_pieces<D>(narrow ? p0 : p0 + warp, narrow ? 1 : kW, p1, row, part, m, l, div, o);
+    join_pieces<D>(narrow ? u.p0 : u.p0 + warp, narrow ? 1 : kW, u.p1, row, part, m, l, div, o);
     if (!narrow) {
       __syncthreads();
       if (lane == 0) sh.m[warp] = m, sh.l[warp] = l, sh.d[warp] = div;
@@ -116,13 +133,14 @@ __device__ __forceinline__ void join_rows(JoinShared<D>& sh, int rows, int nth, 
       }
     }
     const float inv = l > 0.f ? 1.f / div : 0.f;
-    const size_t at = out(row);
-    uint32_t* dst = reinterpret_cast<uint32_t*>(o_all + at * D) + lane * (kV / 2);
+    const int at = u.row0 + i;
+    const size_t out = (size_t)(u.tok + at / g) * heads + u.head + at % g;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(o_all + out * D) + lane * (kV / 2);
     if constexpr (kV == 4)
       *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv));
     else
       *dst = pack_bf16(o[0] * inv, o[1] * inv);
-    if (lse && lane == 0) lse[at] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+    if (lse && lane == 0) lse[out] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
   }
 }
 

@@ -99,7 +99,8 @@ struct AttnIn {
   const __nv_bfloat16* q;
   __nv_bfloat16* o;  // [T, heads, D]
   float* lse;        // [T, heads], or null
-  float* partial;    // workspace
+  float* partial;    // workspace: partial sums
+  void* cuts;        // and, for many rows, before them what each piece cuts (JoinCut, s2_cache_join.cuh)
   int64_t ldq;
   int heads, g;      // query heads, and query heads of a key/value head
   float scale_log2;  // log2(e) / sqrt(D)

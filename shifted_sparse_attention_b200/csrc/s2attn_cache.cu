@@ -6,6 +6,7 @@
 
 #include "../../include/s2attn.h"
 #include "s2_cache.cuh"
+#include "s2_cache_join.cuh"
 #include "s2_kernels.h"
 
 namespace {
@@ -98,13 +99,15 @@ int64_t shared_rows(const s2_cache* cache, const s2_cache_batch* batch, int64_t 
 }
 
 // Whether the call's bytes bound it (s2_cache_attn.cu: a key is read, and unpacked, once for every 16 query rows) or
-// its products (s2_cache_chunk.cu: 128 rows at a time, at 20 to 40 us for the first tile).  One block of rows is the
-// former's always.  Beyond, measured on bf16 rows of 128 channels, us of one and the other: 1 x 30000 keys, 8 heads,
-// 64 rows (10^6 keys times blocks) 59 and 53; 16 x 4000, 32 rows (10^6) 62 and 63, 64 rows (2·10^6) 114 and 68;
-// 1 x 2000, 1 head, 128 rows (16·10^3) 11 and 34.
+// its products (s2_cache_chunk.cu: 128 rows at a time, at 15 to 40 us for the first tiles).  One block of rows is the
+// former's always.  Beyond, keys times key/value heads times blocks of rows decide; us of one and the other, rows of
+// 128 channels: bf16 1 x 60 tokens over 8000 keys, 8 heads (9.7·10^5) 62 and 52, 4 x 150 over 1000, 2 heads (6.9·10^5)
+// 53 and 49, 1 x 400 over 1000, 2 heads (5.6·10^5) 41 and 45; 4 bits 4 x 400 over 1000, 8 heads (4.5·10^6) 230 and 106,
+// 1 x 150 over 8000, 2 heads (1.2·10^6) 60 and 66.
 bool few_rows(const s2_cache* cache, const s2_cache_batch* batch, int64_t heads) {
   const int64_t rows = shared_rows(cache, batch, heads), len = batch->max_len ? batch->max_len : batch->table_width * cache->page_size;
-  return rows <= 16 || (double)batch->seqs * (double)len * (double)cache->heads * (double)((rows + 15) / 16) <= 1e6;
+  const double work = (double)batch->seqs * (double)len * (double)cache->heads * (double)((rows + 15) / 16);
+  return rows <= 16 || work <= (cache->format == S2_CACHE_Q4 ? 1e6 : 7e5);
 }
 
 int launched(int rc, const char* what) {
@@ -203,6 +206,7 @@ int s2attn_cache_attn(const s2_cache* cache, const s2_cache_batch* batch, const 
   in.o = static_cast<__nv_bfloat16*>(o);
   in.lse = lse;
   in.partial = static_cast<float*>(workspace);
+  in.cuts = nullptr;
   in.ldq = ldq;
   in.heads = (int)heads;
   in.g = (int)(heads / cache->heads);
@@ -217,8 +221,10 @@ int s2attn_cache_attn(const s2_cache* cache, const s2_cache_batch* batch, const 
                                             static_cast<cudaStream_t>(stream)),
                     "cache attention");
   }
+  in.cuts = workspace;
+  in.partial = reinterpret_cast<float*>(static_cast<char*>(workspace) + s2::kCutBytes);
   in.pieces = s2::kChunkPieces;
-  in.min_piece = 1024;  // keys: less is not worth a second launch's reading of partial sums
+  in.min_piece = 384;  // keys, 256 of which stand for starting a unit: less is not worth a second launch's reading of partial sums
   const uint64_t S = (uint64_t)cache->page_size, d = (uint64_t)D, blocks = (uint64_t)(cache->pages * cache->heads);
   CUtensorMap tq, tk, tv;
   if ((rc = s2::encode_map(&tq, q, {d, (uint64_t)heads, (uint64_t)batch->tokens}, {d * 2, (uint64_t)ldq * 2},
