@@ -98,29 +98,29 @@ __device__ __forceinline__ uint4 pack8(const float* x) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Codes min(rint(a / s), 15) of a thread's 16 numbers a = x - min, as its 8 bytes.  By the reciprocal, added to
-// 1.5·2^23: the sum's low bits are the rounded quotient, with no conversion (those run at a quarter of the
-// rate), and eight sums' bits added up in their places, less eight times the constant's, are a word.  The product is
-// within 1e-5 of the quotient; where that could round the other way, or s has no reciprocal, the division decides.
+// Codes min(rint(a / s), 15) of a thread's 16 numbers a = x - min, as its 8 bytes.  Numbers of bf16 often lie right
+// between two codes, so the quotient must be the correctly rounded one: from the correctly rounded reciprocal y,
+// q = a y and q + (a - q s) y, the remainder exact (Markstein's theorem), a third of a division's instructions.
+// Added to 1.5·2^23 its low bits are the rounded quotient, with no conversion (those run at a quarter of the rate),
+// and eight sums' bits added up in their places, less eight times the constant's, are a word.
 __device__ __forceinline__ uint2 codes_of(const Row& a, float s) {
   constexpr float kMagic = 12582912.f;        // 0x4b400000
   constexpr uint32_t kBits = 0x4b400000u * 0x11111111u;
-  const float inv = 1.0f / s;
+  const float y = __frcp_rn(s);
+  auto place = [&](float x) -> uint32_t {
+    const float q = x * y;
+    return __float_as_uint(fmaf(fmaf(-q, s, x), y, q) + kMagic);
+  };
   uint32_t w[2];
-  float far = 0.f;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     uint32_t sum = 0u - kBits;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float x = a.lo[4 * h + i], y = a.hi[4 * h + i];
-      const float lo = fmaf(x, inv, kMagic), hi = fmaf(y, inv, kMagic);
-      far = fmax3(far, fabsf(fmaf(x, inv, kMagic - lo)), fabsf(fmaf(y, inv, kMagic - hi)));
-      sum += __float_as_uint(lo) * (1u << (8 * i)) + __float_as_uint(hi) * (16u << (8 * i));
-    }
+    for (int i = 0; i < 4; ++i)
+      sum += place(a.lo[4 * h + i]) * (1u << (8 * i)) + place(a.hi[4 * h + i]) * (16u << (8 * i));
     w[h] = sum;
   }
-  if (!(far <= 0.4999f) || s < 1e-30f) {
+  if (s < 1e-30f) {  // remainders or the reciprocal would leave the range of 32 bits
     w[0] = w[1] = 0u;
     for (int i = 0; i < 8; ++i) {
       const uint32_t lo = (uint32_t)fminf(rintf(__fdiv_rn(a.lo[i], s)), 15.f);

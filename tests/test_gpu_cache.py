@@ -334,6 +334,26 @@ def test_packing_of_flat_and_broken_rows():
         assert (t[0] == -3.0).all() and torch.isnan(t[1:3]).all() and torch.isfinite(t[3]).all()
 
 
+def test_codes_at_borders_and_of_all_sizes():
+    """Rows whose numbers lie right between two codes, and rows from the smallest numbers to large ones: the codes are
+    those of the 32-bit definition, to the last bit."""
+    g = torch.Generator().manual_seed(3)
+    rows = [torch.randint(-200, 200, (200, 128), generator=g).float() * 2.0 ** e for e in (-130, -126, -100, -8, 0, 60, 100)]
+    rows += [torch.arange(128).float()[None] * 0.5 ** k for k in range(6)]
+    x = torch.cat(rows).bfloat16()
+    T = len(x)
+    cache = s2.KVCache.empty(-(-T // 16), 16, 1, 128, bits=4)
+    batch = s2.CacheBatch(torch.arange(-(-T // 16), dtype=torch.int32)[None].cuda(),
+                          torch.tensor([T], dtype=torch.int32).cuda(), torch.tensor([0, T], dtype=torch.int32).cuda(), T)
+    s2.cache_append(cache, batch, x[:, None].cuda(), x[:, None].cuda(), base=0.0)
+    f = x.float()
+    mn, mx = f.amin(-1, keepdim=True), f.amax(-1, keepdim=True)
+    s = ((mx - mn) / 15).bfloat16().float()
+    c = torch.where(s > 0, torch.round((f - mn) / torch.where(s > 0, s, 1.0)), 0.0).clamp(0, 15)
+    assert torch.equal(cache.v.view(-1, 64)[:T].cpu(), ref.join_codes(c))
+    assert torch.equal(cache.v_scale.view(-1, 2)[:T].cpu().float(), torch.cat([s, mn], -1))
+
+
 def test_numbers_out_of_range_are_reported_and_touch_nothing():
     c = ref.Paged([40, 33], 2, 64, 16, 16)
     T = 2
