@@ -190,8 +190,10 @@ struct RowAt {
 // Rows of a token in order: H query heads (none without q), Hkv key heads, Hkv value heads.  Where a row
 // comes from does not depend on its sequence: the first rows are on their way before the tokens are found,
 // and each next row while the last one is worked on.
+// Six CTAs an SM hold 40 registers a thread, enough for bf16 rows (8192 tokens of 32 and 8 heads 139.7 us, with five
+// 141.7); packing needs 48, so five (79.2 us; 82.6 as compiled without a bound, 82.2 with six, which spill).
 template <int D, bool Q4, bool kRotate>
-__global__ void __launch_bounds__(kThreads) s2_cache_append_kernel(const __grid_constant__ CacheArgs c,
+__global__ void __launch_bounds__(kThreads, Q4 ? 5 : 6) s2_cache_append_kernel(const __grid_constant__ CacheArgs c,
                                                                    const __grid_constant__ AppendIn in) {
   constexpr int kHalf = D / 2, kLanes = D / 16, kRows = kThreads / kLanes;
   __shared__ Token tok[kTok];
@@ -289,7 +291,7 @@ __global__ void __launch_bounds__(kThreads) s2_cache_read_kernel(const __grid_co
   __syncthreads();
   const int per_token = 2 * c.heads;
   const int lane = threadIdx.x % kLanes;
-#pragma unroll 2
+#pragma unroll 8
   for (int w = threadIdx.x / kLanes; w < kTokens * per_token; w += kRows) {
     const int x = w / per_token, r = w % per_token;
     if (!tok[x].store) continue;
@@ -341,9 +343,11 @@ template <int D, bool Q4>
 static int read_impl(const CacheArgs& c, void* k_out, void* v_out, cudaStream_t stream) {
   auto* k = static_cast<__nv_bfloat16*>(k_out);
   auto* v = static_cast<__nv_bfloat16*>(v_out);
-  // finding the tokens takes as long as moving a few rows: many to a CTA, as long as that leaves CTAs for all SMs
-  if ((int64_t)c.T * c.heads >= 1 << 16)
-    s2_cache_read_kernel<D, Q4, 16><<<(unsigned)((c.T + 15) / 16), kThreads, 0, stream>>>(c, k, v);
+  // Finding the tokens takes as long as moving a few rows, so a CTA of few heads takes 8 tokens, if that leaves CTAs
+  // for all SMs (8 heads, 8192 tokens in 4 bits: 10.5 us with 8, 11.4 with 4; 32 heads, 8192 tokens: 34.7 with 8 or 4
+  // in 4 bits, 50.6 and 46.9 in bf16; 8 heads, 256 tokens: 4.3 and 3.5).
+  if (c.heads < 16 && (int64_t)c.T * c.heads >= 1 << 16)
+    s2_cache_read_kernel<D, Q4, 8><<<(unsigned)((c.T + 7) / 8), kThreads, 0, stream>>>(c, k, v);
   else
     s2_cache_read_kernel<D, Q4, kTok><<<(unsigned)((c.T + kTok - 1) / kTok), kThreads, 0, stream>>>(c, k, v);
   return (int)cudaGetLastError();
