@@ -68,7 +68,8 @@ enum {
   S2_ERR_UNSUPPORTED = -3, /* valid for the method but not for these kernels (D, G/2 % 128, GPU) */
   S2_ERR_CUDA = -4,        /* a CUDA runtime call failed */
   S2_ERR_TIMEOUT = -5,     /* a kernel gave up waiting on a barrier */
-  S2_ERR_BOUNDS = -6       /* the debug build found an index outside its bounds (see below) */
+  S2_ERR_BOUNDS = -6       /* the debug build found an index outside its bounds (see below), or a cache
+                              batch holds a number out of range */
 };
 
 /* Forward.  Writes o [B,N,H,D] (bf16) and lse [B,H,N] (fp32) for all N rows. */
@@ -270,7 +271,8 @@ int s2attn_graph_gap(const float* lse_s2, const float* lse_full, const void* o_s
  *
  * The cache.  k and v hold `pages` pages of page_size rows for each of `heads`
  * key/value heads, [pages, heads, page_size, ..], contiguous, device memory,
- * 16-byte aligned.  D in {64, 128}, page_size in {16, 32, 64, 128}.
+ * 16-byte aligned.  D in {64, 128}, page_size in {16, 32, 64, 128},
+ * pages * heads < 2^31 and pages * heads * page_size < 2^32.
  *   S2_CACHE_BF16: rows of D bf16; k_scale and v_scale are NULL.
  *   S2_CACHE_Q4:   rows of D/2 bytes, byte j = code(j) | code(j + D/2) << 4, and
  *                  k_scale, v_scale [pages, heads, page_size, 2] bf16 with the
@@ -290,7 +292,8 @@ int s2attn_graph_gap(const float* lse_s2, const float* lse_full, const void* o_s
  * with seq_lens[b] = 0) has no row and sees no key: nothing is stored for it,
  * its o is 0 and its lse -inf.
  * max_new and max_len are the host's bounds of n_b and seq_lens[b]: they choose
- * kernels and their tiling, and no result depends on them.
+ * kernels and their tiling, and no result depends on them.  table_width *
+ * page_size < 2^30.
  * Numbers out of range (a page outside [0, pages), a length beyond the table, a
  * decreasing or too large start) are found by the kernels: nothing outside the
  * buffers is touched, the sequence's results are undefined, and
@@ -332,7 +335,7 @@ typedef struct {
  * then be NULL.  Into a 4-bit cache, each row x (rounded to bf16) gets
  * min = min_j x_j, scale = bf16((max_j x_j - min) / 15), code_j =
  * min(rint((x_j - min) / scale), 15), 0 when scale is 0; a row that holds an
- * infinity or a NaN reads back as NaN.  Pages that other sequences share must
+ * infinity or a NaN, or whose numbers lie 2^128 apart, reads back as NaN.  Pages that other sequences share must
  * not be written. */
 int s2attn_cache_append(const s2_cache* cache, const s2_cache_batch* batch, const void* q, int64_t ldq,
                         const void* k, int64_t ldk, const void* v, int64_t ldv, void* q_out, int64_t heads,
@@ -346,7 +349,8 @@ int s2attn_cache_read(const s2_cache* cache, const s2_cache_batch* batch, void* 
 
 /* Attention of the new tokens over the cache (their own rows included: append
  * first).  q [tokens, heads, D] bf16, rows of a token ldq elements apart, rotated;
- * heads a multiple of the cache's, query head h reads key/value head
+ * heads a multiple of the cache's (at most 128 to each of its heads, and
+ * tokens * heads < 2^31), query head h reads key/value head
  * h / (heads / cache heads).  For the token at place p of its sequence
  *   o = sum_{j <= p} softmax_j(q·k_j / sqrt(D)) v_j,  lse = ln sum_{j <= p} exp(..),
  * o [tokens, heads, D] bf16, lse [tokens, heads] fp32 or NULL.  Results do not
@@ -413,9 +417,10 @@ int s2attn_debug_adjacency(int64_t N, int64_t G, int64_t n_valid, int variant, i
 int s2attn_debug_adjacency_docs(int64_t N, int64_t G, int64_t n_valid, int variant, int head_class,
                                 const int32_t* doc_bounds, int format, void* out, void* stream);
 
-/* Synchronizes `stream` and reports (then clears) a kernel timeout, or a
- * bounds violation of the debug build, recorded on the current device since
- * the last check: S2_OK, S2_ERR_TIMEOUT or S2_ERR_BOUNDS (the latter first). */
+/* Synchronizes `stream` and reports (then clears) a kernel timeout, a bounds
+ * violation of the debug build, or a cache batch's number out of range, recorded
+ * on the current device since the last check: S2_OK, S2_ERR_TIMEOUT or
+ * S2_ERR_BOUNDS (the latter first). */
 int s2attn_check_status(void* stream);
 
 /* Bounds-checked build.  The library can also be built as

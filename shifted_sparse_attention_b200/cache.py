@@ -162,7 +162,7 @@ def _rows(name, t, cache, batch, heads):
     row, head, one = t.stride()
     if one != 1 or (head != cache.dim and heads > 1):
         raise ValueError("the heads of a token of %s must lie side by side" % name)
-    return row if batch.tokens > 1 else max(row, heads * cache.dim)
+    return row if batch.tokens > 1 else heads * cache.dim  # (of one token any stride will do)
 
 
 def _query_heads(q):

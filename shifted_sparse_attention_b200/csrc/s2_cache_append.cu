@@ -134,7 +134,7 @@ __device__ __forceinline__ uint2 codes_of(const Row& a, float s) {
 __device__ __forceinline__ __nv_bfloat162 as_pair(uint32_t x) { return *reinterpret_cast<__nv_bfloat162*>(&x); }
 
 // Packs a row held by LANES lanes (bf16 values) to 4 bits: this lane's 8 bytes and the row's (scale, min).
-// A row with a NaN or an infinity reads back as NaN.
+// A row with a NaN or an infinity, or whose scale is none, reads back as NaN.
 template <int LANES>
 __device__ __forceinline__ void pack_row(const uint4& lo, const uint4& hi, uint2& codes, uint32_t& pair) {
   // extremes of pairs of numbers; 0 times a number that is none is none
@@ -160,6 +160,7 @@ __device__ __forceinline__ void pack_row(const uint4& lo, const uint4& hi, uint2
   __nv_bfloat16 sb = __float2bfloat16_rn(__fdiv_rn(mx - mn, 15.0f));
   __nv_bfloat16 mb = __float2bfloat16_rn(mn);  // exact: the row is bf16
   const float s = __bfloat162float(sb);
+  good &= s < INFINITY;
   codes = make_uint2(0u, 0u);
   if (good && s > 0.f) {
     Row x;

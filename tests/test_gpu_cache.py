@@ -494,3 +494,31 @@ def test_calls_on_other_streams():
     torch.cuda.synchronize()
     assert all(torch.equal(o, want) for o in outs)
     s2.check_status()
+
+
+def test_one_token_of_any_stride():
+    # the rows of one token are nowhere apart: what the tensor says their distance is does not matter
+    c = ref.Paged([77], 2, 128, 32, 16)
+    batch, q, kv = batch_of(c, [1], plain=True), torch.randn(1, 4, 128).bfloat16(), torch.randn(1, 2, 128).bfloat16()
+
+    def odd(t):
+        return torch.as_strided(t.cuda(), t.shape, (3, 128, 1))
+
+    a, b = on_gpu(c), on_gpu(c)
+    assert torch.equal(s2.cache_append(a, batch, odd(kv), odd(kv), odd(q)),
+                       s2.cache_append(b, batch, kv.cuda(), kv.cuda(), q.cuda()))
+    for x, y in ((a.k, b.k), (a.v, b.v)):  # as bits: rows that hold nothing hold NaN
+        assert torch.equal(x.view(torch.int16), y.view(torch.int16))
+    assert torch.equal(s2.cache_attention(a, batch, odd(q)), s2.cache_attention(b, batch, q.cuda()))
+
+
+def test_packing_of_rows_wider_than_32_bits():
+    cache = s2.KVCache.empty(1, 16, 1, 64, bits=4)
+    cache.k.fill_(255)
+    batch = s2.CacheBatch(torch.zeros(1, 1, dtype=torch.int32).cuda(), torch.tensor([2], dtype=torch.int32).cuda(),
+                          torch.tensor([0, 2], dtype=torch.int32).cuda(), 2)
+    x = torch.randn(2, 1, 64).bfloat16()
+    x[0, 0, 3], x[0, 0, 40] = 3e38, -3e38  # finite, but their distance is not
+    s2.cache_append(cache, batch, x.cuda(), x.cuda(), base=0.0)
+    for t in s2.cache_read(cache, batch):
+        assert torch.isnan(t[0]).all() and torch.isfinite(t[1]).all()
