@@ -4,7 +4,8 @@
 // A page holds S rows (S = 16, 32, 64 or 128) of every key/value head, head
 // by head: row (page, h, slot) starts at ((page·Hkv + h)·S + slot)·rowbytes, so
 // the rows that one attention unit streams, a head's S rows of a page, are
-// contiguous (4 KB and more in bf16).  All row numbers are 64-bit.
+// contiguous (4 KB and more in bf16).  Rows are fewer than 2^32; offsets are
+// 64-bit.
 //
 // 4-bit rows: byte j holds the code of channel j in its low half and that of
 // channel j + D/2 in its high half; a row stands for min + scale·code, scale

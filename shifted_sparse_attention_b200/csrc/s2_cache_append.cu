@@ -3,9 +3,11 @@
 //
 // Append: the new keys (and, beside them, the queries) are rotated to their
 // positions as in s2_rope.cu and keys and values go to their rows of the
-// cache, in bf16 or packed to 4 bits, in one pass over q, k and v: the pass
-// is bound by HBM (or, for a few tokens, by latency), so the rotation and the
-// packing ride along for free and no rotated copy of k is written.
+// cache, in bf16 or packed to 4 bits, in one pass over q, k and v, and no
+// rotated copy of k is written.  HBM bounds the pass into bf16 rows, the
+// rotation rides along (34,500 tokens of 32 + 8 heads of 128 channels, 848 MB:
+// 140 us); into 4-bit rows packing's instructions do (issue slots 73% taken;
+// 18,900 tokens 79 us, HBM's part 62), for a few tokens latency does.
 //
 // Work: a CTA takes kTok tokens.  Their places, pages and angles come first
 // (one warp per token finds its sequence, one thread per (token, pair) its
@@ -191,8 +193,9 @@ struct RowAt {
 // Rows of a token in order: H query heads (none without q), Hkv key heads, Hkv value heads.  Where a row
 // comes from does not depend on its sequence: the first rows are on their way before the tokens are found,
 // and each next row while the last one is worked on.
-// Six CTAs an SM hold 40 registers a thread, enough for bf16 rows (8192 tokens of 32 and 8 heads 139.7 us, with five
-// 141.7); packing needs 48, so five (79.2 us; 82.6 as compiled without a bound, 82.2 with six, which spill).
+// Six CTAs an SM hold 40 registers a thread, enough for bf16 rows (34,500 tokens of 32 and 8 heads 139.7 us, with five
+// 141.7, the HBM's 129); packing needs 48, so five (18,900 tokens 79.2 us; 82.6 as compiled without a bound, 82.2 with
+// six, which spill).
 template <int D, bool Q4, bool kRotate>
 __global__ void __launch_bounds__(kThreads, Q4 ? 5 : 6) s2_cache_append_kernel(const __grid_constant__ CacheArgs c,
                                                                    const __grid_constant__ AppendIn in) {

@@ -32,6 +32,10 @@
 //   weights are rounded to bf16 for the product (2^-8 of each at most); O is
 //   divided by the sum of the rounded ones where that is to be had (bf16 rows),
 //   so that it stays a mean of values, and lse comes from the unrounded sum.
+// Measured (D 128): 64 sequences of 17 to 8192 keys, 32 heads on 8 key heads,
+// 1.09 GB, 172 us, 0.96 of the measured copy rate; one of 32768 keys 24.8 us
+// (HBM's part 20.5); 4 bits, 48 sequences of 33 to 4096 keys, 32 key heads, 433 MB,
+// 109 us (HBM's part 66), where unpacking bounds it (ALU 57%, issue 56%).
 #include <climits>
 
 #include <cuda_bf16.h>
