@@ -9,7 +9,7 @@
 // 140 us); into 4-bit rows packing's instructions do (issue slots 73% taken;
 // 18,900 tokens 79 us, HBM's part 62), for a few tokens latency does.
 //
-// Work: a CTA takes kTok tokens.  Their places, pages and angles come first
+// Work: a CTA takes one token, or 4.  Their places, pages and angles come first
 // (one warp per token finds its sequence, one thread per (token, pair) its
 // angle), then D/16 lanes take a row of one head: lane i the channels
 // [8i, 8i + 8) and [D/2 + 8i, D/2 + 8i + 8), which are 8 rotation pairs and, in
@@ -32,7 +32,10 @@ namespace s2 {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kTok = 4;  // tokens of a CTA
+// Calls of up to this many tokens give each a CTA: all of them are resident at once, and a token's rows go by in the
+// fewest turns (32 + 8 heads, 64 tokens: append 4.3 us with 1 token to a CTA, 6.7 with 4; 600 tokens 6.1 and 7.0).
+// Beyond, what a CTA does before its rows is shared by 4 tokens (2400 tokens in 4 bits: 15.1 us, 18.9 with 1).
+constexpr int kLoneTokens = 5 * 148;
 
 // Sequence of packed token t: the number of sequences whose new tokens end at or before t.
 // Whole warp; B when no sequence holds it.
@@ -196,9 +199,9 @@ struct RowAt {
 // Six CTAs an SM hold 40 registers a thread, enough for bf16 rows (34,500 tokens of 32 and 8 heads 139.7 us, with five
 // 141.7, the HBM's 129); packing needs 48, so five (18,900 tokens 79.2 us; 82.6 as compiled without a bound, 82.2 with
 // six, which spill).
-template <int D, bool Q4, bool kRotate>
-__global__ void __launch_bounds__(kThreads, Q4 ? 5 : 6) s2_cache_append_kernel(const __grid_constant__ CacheArgs c,
-                                                                   const __grid_constant__ AppendIn in) {
+template <int D, bool Q4, bool kRotate, int kTok>
+__global__ void __launch_bounds__(kThreads, Q4 ? 5 : 6)
+    s2_cache_append_kernel(const __grid_constant__ CacheArgs c, const __grid_constant__ AppendIn in) {
   constexpr int kHalf = D / 2, kLanes = D / 16, kRows = kThreads / kLanes;
   __shared__ Token tok[kTok];
   __shared__ __align__(16) float2 cs[kTok][kHalf];
@@ -328,32 +331,39 @@ __global__ void __launch_bounds__(kThreads) s2_cache_read_kernel(const __grid_co
   }
 }
 
-template <int D, bool Q4>
+template <int D, bool Q4, int kTok>
 static int append_impl(const CacheArgs& c, const AppendIn& in, bool rotate, cudaStream_t stream) {
   const unsigned grid = (unsigned)((c.T + kTok - 1) / kTok);
   if (rotate)
-    s2_cache_append_kernel<D, Q4, true><<<grid, kThreads, 0, stream>>>(c, in);
+    s2_cache_append_kernel<D, Q4, true, kTok><<<grid, kThreads, 0, stream>>>(c, in);
   else
-    s2_cache_append_kernel<D, Q4, false><<<grid, kThreads, 0, stream>>>(c, in);
+    s2_cache_append_kernel<D, Q4, false, kTok><<<grid, kThreads, 0, stream>>>(c, in);
   return (int)cudaGetLastError();
 }
 
+template <int D, bool Q4>
+static int append_tokens(const CacheArgs& c, const AppendIn& in, bool rotate, cudaStream_t stream) {
+  return c.T <= kLoneTokens ? append_impl<D, Q4, 1>(c, in, rotate, stream) : append_impl<D, Q4, 4>(c, in, rotate, stream);
+}
+
 int launch_cache_append(const CacheArgs& c, const AppendIn& in, int D, bool q4, bool rotate, cudaStream_t stream) {
-  if (D == 64) return q4 ? append_impl<64, true>(c, in, rotate, stream) : append_impl<64, false>(c, in, rotate, stream);
-  return q4 ? append_impl<128, true>(c, in, rotate, stream) : append_impl<128, false>(c, in, rotate, stream);
+  if (D == 64) return q4 ? append_tokens<64, true>(c, in, rotate, stream) : append_tokens<64, false>(c, in, rotate, stream);
+  return q4 ? append_tokens<128, true>(c, in, rotate, stream) : append_tokens<128, false>(c, in, rotate, stream);
 }
 
 template <int D, bool Q4>
 static int read_impl(const CacheArgs& c, void* k_out, void* v_out, cudaStream_t stream) {
   auto* k = static_cast<__nv_bfloat16*>(k_out);
   auto* v = static_cast<__nv_bfloat16*>(v_out);
-  // Finding the tokens takes as long as moving a few rows, so a CTA of few heads takes 8 tokens, if that leaves CTAs
-  // for all SMs (8 heads, 8192 tokens in 4 bits: 10.5 us with 8, 11.4 with 4; 32 heads, 8192 tokens: 34.7 with 8 or 4
-  // in 4 bits, 50.6 and 46.9 in bf16; 8 heads, 256 tokens: 4.3 and 3.5).
-  if (c.heads < 16 && (int64_t)c.T * c.heads >= 1 << 16)
+  // As for append (32 heads, 64 tokens in 4 bits: 3.6 us with 1 token to a CTA, 6.1 with 4; 8 heads, 2400 tokens 6.9
+  // and 5.4), and CTAs of few heads take 8 tokens, if that leaves CTAs for all SMs (8 heads, 8192 tokens in 4 bits:
+  // 10.5 us with 8, 11.4 with 4; 32 heads, 8192 tokens: 34.7 with 8 or 4 in 4 bits, 50.6 and 46.9 in bf16).
+  if (c.T <= kLoneTokens)
+    s2_cache_read_kernel<D, Q4, 1><<<(unsigned)c.T, kThreads, 0, stream>>>(c, k, v);
+  else if (c.heads < 16 && (int64_t)c.T * c.heads >= 1 << 16)
     s2_cache_read_kernel<D, Q4, 8><<<(unsigned)((c.T + 7) / 8), kThreads, 0, stream>>>(c, k, v);
   else
-    s2_cache_read_kernel<D, Q4, kTok><<<(unsigned)((c.T + kTok - 1) / kTok), kThreads, 0, stream>>>(c, k, v);
+    s2_cache_read_kernel<D, Q4, 4><<<(unsigned)((c.T + 3) / 4), kThreads, 0, stream>>>(c, k, v);
   return (int)cudaGetLastError();
 }
 

@@ -313,6 +313,16 @@ def test_append_and_read(bits, D, H, Hkv, S, lens, news):
 
 
 @pytest.mark.parametrize("bits", [16, 4])
+@pytest.mark.parametrize("D,H,Hkv,S,lens,news", [
+    (128, 4, 2, 64, [900, 17, 0, 64], [690, 17, 0, 33]),  # the last call of one token to a CTA,
+    (128, 4, 2, 64, [900, 17, 0, 64], [691, 17, 0, 33]),  # and the first of several
+    (64, 8, 8, 16, [8300, 90], [8200, 3]),
+])
+def test_append_and_read_of_many_tokens(bits, D, H, Hkv, S, lens, news):
+    check_append(lens, news, H, Hkv, D, S, bits, seed=news[0])
+
+
+@pytest.mark.parametrize("bits", [16, 4])
 def test_append_at_given_positions_and_unrotated(bits):
     pos = torch.tensor([0, 1, 8191, 99999, 1000000, 2 ** 31 - 1, 7])
     check_append([40, 9], [4, 3], 4, 2, 128, 32, bits, base=500000.0, scale=0.25, positions=pos)
