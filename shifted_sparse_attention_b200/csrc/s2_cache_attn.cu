@@ -17,6 +17,9 @@
 //   into equal pieces, one per CTA, so sequences of any lengths load all SMs
 //   alike; a unit cut by a border leaves partial sums (max, sum, O) that
 //   a second launch adds up in a fixed order.
+//   Short units (cut_units below) are not cut: a CTA takes one, or a cluster's
+//   CTAs take equal parts of one and add their sums up through each other's
+//   shared memory, in one launch.
 // - a warp takes every fourth step of its CTA's piece by itself: loads go from
 //   global memory straight to the registers that mma.sync reads as its A
 //   operand (S^T = K Q^T and O^T = V^T P^T, so keys fill the 16-row side and
@@ -81,6 +84,22 @@ __device__ __forceinline__ uint32_t ld_stream4(const void* p) {
   uint32_t v;
   asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(v) : "l"(p));
   return v;
+}
+
+// Shared memory of the cluster's CTA `rank` at this CTA's address.
+__device__ __forceinline__ float4 ld_cluster16(const void* p, int rank) {
+  float4 v;
+  uint32_t at;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(at)
+               : "memory");
+  return v;
+}
+// All threads of all of the cluster's CTAs; what they wrote before is seen by all after.
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
 }
 
 // Registers of one 16-key block of K and of V in the order the products take them.
@@ -193,11 +212,14 @@ __host__ __device__ constexpr int step_blocks() { return Q4 ? 2 : 1; }
 template <bool Q4, int NR, int W>
 __host__ __device__ constexpr int ctas_per_sm() { return (NR == 2 ? 8 : Q4 ? 16 : 12) / W; }
 
+constexpr int kMaxCluster = 8;
+
 template <int D, int NR, int W>
 struct DecodeShared {
   long long line[W + 2];
   long long x0, x1;  // the CTA's piece [x0, x1) of the line: here and not in registers, which the keys need
   float m[W][8 * NR], l[W][8 * NR], div[W][8 * NR];  // maximum, sum of weights, what O is divided by
+  alignas(16) float4 all[8 * NR];                    // the same of the CTA, for its cluster (O is then in o[0])
   alignas(16) float o[W][8 * NR][D + 4];
 };
 
@@ -215,17 +237,19 @@ __global__ void __launch_bounds__(W * 32, ctas_per_sm<Q4, NR, W>())
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, r = lane / 4, cc = lane % 4;
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join may start its own set-up
-  // cut units: each takes its steps of the line; whole units: one point each, and a CTA takes one unit
+  // cut units: each takes its steps of the line; whole units: one point each, and a CTA, or the CTAs of a cluster
+  // together, take one unit
   const bool cut = in.pieces > 0;
   auto weight = [&](int i) { return seq_steps<NR, W>(c, in, i, kStep, cut); };
   int b;
   long long seq_first;
-  const Line line = find_piece<kThreads>(c.B, cut ? in.pieces : INT_MAX, in.min_piece, blockIdx.x, sh.line, weight, b,
-                                         seq_first);
-  if (line.piece * blockIdx.x >= line.total) return;
+  const int index = (int)(blockIdx.x / (unsigned)in.cluster), rank = (int)(blockIdx.x % (unsigned)in.cluster);
+  const Line line =
+      find_piece<kThreads>(c.B, cut ? in.pieces : INT_MAX, in.min_piece, index, sh.line, weight, b, seq_first);
+  if (line.piece * index >= line.total) return;  // (all of a cluster's CTAs do)
   if (threadIdx.x == 0) {
-    sh.x0 = line.piece * blockIdx.x;
-    sh.x1 = min(line.piece * (blockIdx.x + 1), line.total);
+    sh.x0 = line.piece * index;
+    sh.x1 = min(line.piece * (index + 1), line.total);
   }
   __syncthreads();
   // a lane's place in a block of 16 rows
@@ -248,11 +272,12 @@ __global__ void __launch_bounds__(W * 32, ctas_per_sm<Q4, NR, W>())
     const long long unit = quotient(x - seq_first, span);
     const long long unit_first = seq_first + unit * span + head;  // of its steps
     const int h = (int)quotient(unit, blocks), rb = (int)(unit - (long long)h * blocks);
-    const int k0 = (int)max(0LL, x - unit_first);
-    const int k1 = cut ? (int)min((long long)steps, sh.x1 - unit_first) : steps;
+    const int k0 = cut ? (int)max(0LL, x - unit_first) : (int)((unsigned)(steps * rank) / (unsigned)in.cluster);
+    const int k1 = cut ? (int)min((long long)steps, sh.x1 - unit_first)
+                       : (int)((unsigned)(steps * (rank + 1)) / (unsigned)in.cluster);
     x = unit_first + (cut ? steps : 1);
-    if (k1 <= k0) continue;
-    const int slot = k0 == 0 && k1 == steps ? -1 : 2 * (int)blockIdx.x + (unit_first < sh.x0 ? 0 : 1);  // -1: whole
+    if (cut && k1 <= k0) continue;
+    const int slot = !cut || (k0 == 0 && k1 == steps) ? -1 : 2 * (int)blockIdx.x + (unit_first < sh.x0 ? 0 : 1);  // -1: whole
 
     // ---------------------------------------------------------- query rows
     // B operand of S^T: lane (r, cc) holds row r's channels as load_keys orders them
@@ -577,7 +602,10 @@ __global__ void __launch_bounds__(W * 32, ctas_per_sm<Q4, NR, W>())
         div += sh.div[w][row] * f;
         o.x += v.x * f, o.y += v.y * f, o.z += v.z * f, o.w += v.w * f;
       }
-      if (slot < 0) {
+      if (in.cluster > 1) {
+        *reinterpret_cast<float4*>(&sh.o[0][row][d]) = o;
+        if (d == 0) sh.all[row] = make_float4(mm, ll, div, 0.f);
+      } else if (slot < 0) {
         const int at = rb * kRows + row;
         const size_t out = (size_t)(seq.first + at / in.g) * in.heads + h * in.g + at % in.g;
         const float inv = ll > 0.f ? 1.f / div : 0.f;
@@ -590,6 +618,39 @@ __global__ void __launch_bounds__(W * 32, ctas_per_sm<Q4, NR, W>())
       }
     }
     __syncthreads();
+    // ---------------------------------------------------------- and the cluster's CTAs', each a part of the rows
+    if (in.cluster > 1) {
+      cluster_sync();
+      for (int i = rank * kThreads + threadIdx.x; i < rows_here * (D / 4); i += in.cluster * kThreads) {
+        const int row = i / (D / 4), d = 4 * (i % (D / 4));
+        float4 ml[kMaxCluster], v[kMaxCluster];
+#pragma unroll
+        for (int p = 0; p < kMaxCluster; ++p) {
+          ml[p] = make_float4(-INFINITY, 0.f, 0.f, 0.f);
+          v[p] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (p < in.cluster) ml[p] = ld_cluster16(&sh.all[row], p), v[p] = ld_cluster16(&sh.o[0][row][d], p);
+        }
+        float mm = -INFINITY, ll = 0.f, div = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int p = 0; p < kMaxCluster; ++p) mm = fmaxf(mm, ml[p].x);
+#pragma unroll
+        for (int p = 0; p < kMaxCluster; ++p) {
+          const float f = ml[p].x == -INFINITY ? 0.f : ex2(ml[p].x - mm);
+          ll = fmaf(ml[p].y, f, ll);
+          div = fmaf(ml[p].z, f, div);
+          o.x = fmaf(v[p].x, f, o.x), o.y = fmaf(v[p].y, f, o.y);
+          o.z = fmaf(v[p].z, f, o.z), o.w = fmaf(v[p].w, f, o.w);
+        }
+        const int at = rb * kRows + row;
+        const size_t out = (size_t)(seq.first + at / in.g) * in.heads + h * in.g + at % in.g;
+        const float inv = ll > 0.f ? 1.f / div : 0.f;
+        *reinterpret_cast<uint2*>(in.o + out * D + d) =
+            make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+        if (in.lse && d == 0) in.lse[out] = ll > 0.f ? (mm + log2f(ll)) * 0.69314718055994531f : -INFINITY;
+      }
+      cluster_sync();  // nobody leaves while its sums are being read
+    }
   }
 }
 
@@ -633,10 +694,34 @@ __global__ void __launch_bounds__(kJoinThreads) s2_cache_join_kernel(const __gri
   join_rows<D>(sh, u, in.partial, kRows, in.g, in.heads, [](int i) { return i; }, in.o, in.lse);
 }
 
+// CTAs to a whole unit, so that few units fill the GPU: as many as are resident at once, up to 8, with 64 keys each at
+// least (32 units of 200 keys in bf16: 1 to 8 CTAs 7.0, 7.2, 6.3, 6.8 us).
+static int cluster_of(int64_t units, int64_t max_len, int resident) {
+  int cs = 1;
+  while (2 * cs <= kMaxCluster && 2 * cs * units <= resident && max_len >= 64 * 2 * cs) cs *= 2;
+  return cs;
+}
+
+// Whether units are cut and joined in a second launch, or whole ones taken by clusters.  The latter needs one launch and
+// no partial sums in memory, but the longest unit sets its time, and only a bound of the lengths is known: up to 256
+// keys a CTA it is no slower than the former is at half the bound on the average (us whole and cut: 32 units of 513
+// keys 7.6 and 9.5, of 1024 8.0 and 9.7, of 2048 9.9 and 12.8, of 4096 14.1 and 16.2; 8 units of 2048 8.6 and 8.7, of
+// 4096 11.3 and 9.8; 128 units, two CTAs each, of 513 10.7 and 13.4, of 2048 25.3 and 25.4).
+static bool cut_units(int64_t max_len, int cluster) {
+  return max_len == 0 || max_len > 256 * (cluster > 2 ? cluster : 2);
+}
+
 template <int D, bool Q4, int NR, int W>
-static int decode_impl(const CacheArgs& c, const AttnIn& in0, bool cut, cudaStream_t stream) {
+static int decode_impl(const CacheArgs& c, const AttnIn& in0, int64_t max_len, cudaStream_t stream) {
   AttnIn in = in0;
-  in.pieces = cut ? 148 * ctas_per_sm<Q4, NR, W>() : 0;
+  // units at most: every sequence rounds its rows up to blocks
+  const int64_t rows = (int64_t)c.T * in.g / (8 * NR) + (c.T < c.B ? c.T : c.B);
+  const int64_t units = c.heads * (c.starts ? rows : (int64_t)c.B * ((in.g + 8 * NR - 1) / (8 * NR)));
+  constexpr int kResident = 148 * ctas_per_sm<Q4, NR, W>();
+  in.cluster = cluster_of(units, max_len, kResident);
+  const bool cut = cut_units(max_len, in.cluster);
+  if (cut) in.cluster = 1;
+  in.pieces = cut ? kResident : 0;
   in.min_piece = cut ? unit_steps<W>() + W : 1;  // a step for each warp
   constexpr int kBytes = (int)sizeof(DecodeShared<D, NR, W>);
   cudaError_t e;
@@ -644,34 +729,42 @@ static int decode_impl(const CacheArgs& c, const AttnIn& in0, bool cut, cudaStre
     e = cudaFuncSetAttribute(s2_cache_decode_kernel<D, Q4, NR, W>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
     if (e != cudaSuccess) return (int)e;
   }
-  // units at most: every sequence rounds its rows up to blocks
-  const int64_t rows = (int64_t)c.T * in.g / (8 * NR) + (c.T < c.B ? c.T : c.B);
-  const int64_t units = c.heads * (c.starts ? rows : (int64_t)c.B * ((in.g + 8 * NR - 1) / (8 * NR)));
   if (!cut && units >= (int64_t(1) << 31)) return (int)cudaErrorInvalidConfiguration;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute at[1];
+  cfg.stream = stream;
+  cfg.attrs = at;
+  if (in.cluster > 1) {
+    cfg.gridDim = dim3((unsigned)(units * in.cluster));
+    cfg.blockDim = dim3(W * 32);
+    cfg.dynamicSmemBytes = kBytes;
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = (unsigned)in.cluster;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.numAttrs = 1;
+    return (int)cudaLaunchKernelEx(&cfg, s2_cache_decode_kernel<D, Q4, NR, W>, c, in);
+  }
   s2_cache_decode_kernel<D, Q4, NR, W><<<(unsigned)(cut ? in.pieces : units), W * 32, kBytes, stream>>>(c, in);
   e = cudaGetLastError();
   if (e != cudaSuccess || !cut) return (int)e;
-  cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(in.pieces - 1);
   cfg.blockDim = dim3(kJoinThreads);
-  cfg.stream = stream;
-  cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
   cfg.numAttrs = 1;
   return (int)cudaLaunchKernelEx(&cfg, s2_cache_join_kernel<D, Q4, NR, W>, c, in);
 }
 
 template <int D, bool Q4>
-static int decode_rows(const CacheArgs& c, const AttnIn& in, int rows, bool cut, cudaStream_t stream) {
-  return rows <= 8 ? decode_impl<D, Q4, 1, 4>(c, in, cut, stream) : decode_impl<D, Q4, 2, 4>(c, in, cut, stream);
+static int decode_rows(const CacheArgs& c, const AttnIn& in, int rows, int64_t max_len, cudaStream_t stream) {
+  return rows <= 8 ? decode_impl<D, Q4, 1, 4>(c, in, max_len, stream) : decode_impl<D, Q4, 2, 4>(c, in, max_len, stream);
 }
 
-int launch_cache_decode(const CacheArgs& c, const AttnIn& in, int D, bool q4, int rows, bool cut, cudaStream_t stream) {
+int launch_cache_decode(const CacheArgs& c, const AttnIn& in, int D, bool q4, int rows, int64_t max_len,
+                        cudaStream_t stream) {
   if (D == 64)
-    return q4 ? decode_rows<64, true>(c, in, rows, cut, stream) : decode_rows<64, false>(c, in, rows, cut, stream);
-  return q4 ? decode_rows<128, true>(c, in, rows, cut, stream) : decode_rows<128, false>(c, in, rows, cut, stream);
+    return q4 ? decode_rows<64, true>(c, in, rows, max_len, stream) : decode_rows<64, false>(c, in, rows, max_len, stream);
+  return q4 ? decode_rows<128, true>(c, in, rows, max_len, stream) : decode_rows<128, false>(c, in, rows, max_len, stream);
 }
 
 size_t cache_decode_partial_bytes(int D) { return (size_t)2 * kDecodePieces * 16 * (D + 4) * sizeof(float); }

@@ -105,15 +105,16 @@ struct AttnIn {
   int heads, g;      // query heads, and query heads of a key/value head
   float scale_log2;  // log2(e) / sqrt(D)
   int pieces, min_piece;
+  int cluster;       // CTAs that share a unit where units are not cut
 };
 
 constexpr int kDecodePieces = 592;  // CTAs of the decode kernel: 4 on each of 148 SMs
 
 int launch_cache_append(const CacheArgs& c, const AppendIn& in, int D, bool q4, bool rotate, cudaStream_t stream);
 int launch_cache_read(const CacheArgs& c, int D, bool q4, void* k_out, void* v_out, cudaStream_t stream);
-// rows: query rows of a unit at most, as far as the caller knows (a choice of tile only); cut: units may be shared by
-// CTAs, and are joined in a second launch
-int launch_cache_decode(const CacheArgs& c, const AttnIn& in, int D, bool q4, int rows, bool cut,
+// rows, max_len: query rows of a unit and a sequence's keys at most, as far as the caller knows (max_len 0: not at all);
+// they choose tiles and how units are shared out only
+int launch_cache_decode(const CacheArgs& c, const AttnIn& in, int D, bool q4, int rows, int64_t max_len,
                         cudaStream_t stream);
 size_t cache_decode_partial_bytes(int D);
 

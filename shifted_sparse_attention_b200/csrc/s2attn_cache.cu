@@ -214,10 +214,7 @@ int s2attn_cache_attn(const s2_cache* cache, const s2_cache_batch* batch, const 
   const bool q4 = cache->format == S2_CACHE_Q4;
   if (few_rows(cache, batch, heads)) {
     const int64_t rows = shared_rows(cache, batch, heads);
-    // Short sequences are not worth cutting: 32 heads of 200 keys took 6.2 us whole and 8.3 cut and joined (and the
-    // host a launch less), of 513 keys 8.5 and 7.8, of 2048 20 and 10.
-    const bool cut = !batch->max_len || batch->max_len > 512;
-    return launched(s2::launch_cache_decode(a, in, (int)D, q4, rows > 16 ? 16 : (int)rows, cut,
+    return launched(s2::launch_cache_decode(a, in, (int)D, q4, rows > 16 ? 16 : (int)rows, batch->max_len,
                                             static_cast<cudaStream_t>(stream)),
                     "cache attention");
   }

@@ -82,6 +82,20 @@ def test_whole_units_of_uneven_batches(bits):
 
 
 @pytest.mark.parametrize("bits", [16, 4])
+@pytest.mark.parametrize("D,H,Hkv,lens,news", [  # how many units there are decides how many CTAs share one
+    (128, 4, 1, [2048], [1]),
+    (128, 32, 32, [513], [1]),
+    (64, 24, 2, [1900, 0, 1, 70, 15], [2, 1, 1, 0, 3]),       # blocks of 16 rows, some of them of no token
+    (128, 4, 4, [1000, 64, 0, 1, 512, 333, 17, 900, 2, 5], [1, 2, 1, 1, 1, 1, 1, 1, 1, 1]),
+    (64, 8, 8, [(97 * i) % 513 for i in range(20)], [1] * 20),
+])
+def test_whole_units_shared_by_clusters(bits, D, H, Hkv, lens, news):
+    c = ref.Paged(lens, Hkv, D, 16, bits, seed=H + lens[0])
+    for max_len in (max(lens), 130):  # 130: longer than the host knows
+        check_attention(c, news, H, max_new=max(news), max_len=max_len)
+
+
+@pytest.mark.parametrize("bits", [16, 4])
 @pytest.mark.parametrize("D", [128, 64])
 @pytest.mark.parametrize("H,Hkv", [(7, 1), (16, 1), (17, 1), (40, 2), (12, 4)])
 def test_heads_shared_by_key_heads(bits, D, H, Hkv):
