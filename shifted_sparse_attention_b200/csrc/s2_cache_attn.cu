@@ -691,7 +691,7 @@ __global__ void __launch_bounds__(kJoinThreads) s2_cache_join_kernel(const __gri
   }
   // every CTA waits, also one with nothing to do: the stream's next launch counts on this one's end alone
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  join_rows<D>(sh, u, in.partial, kRows, in.g, in.heads, [](int i) { return i; }, in.o, in.lse);
+  join_rows<D>(sh, u, in.partial, kRows, in.g, in.heads, in.o, in.lse);
 }
 
 // CTAs to a whole unit, so that few units fill the GPU: as many as are resident at once, up to 8, with 64 keys each at

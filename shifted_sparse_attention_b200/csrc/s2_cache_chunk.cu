@@ -32,6 +32,8 @@
 // chain bounds it (tensor pipe 56%).  4 bits, three chunks of 260 to 1000
 // tokens over 3000 to 12000 keys 353 us; as bf16 pages 245: the difference is
 // the softmax's work on each key's scale and min.
+#include <climits>
+
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -233,6 +235,34 @@ __device__ __forceinline__ void load_pairs(Pairs8& v, uint32_t at) {
         "=f"(v.p[3].x), "=f"(v.p[3].y), "=f"(v.p[3].z), "=f"(v.p[3].w)
       : "r"(at)
       : "memory");
+}
+
+// Partial sums lie as float4 [slot][query tile][channels / 4, then maximum, sum, divisor][row]: a warp's 32 rows write
+// and read 512 bytes side by side.  (Row by row, the 32 lines of each store took 5 us a segment.)
+template <int D>
+__device__ __forceinline__ size_t partial_at(int slot, int x, int c4) {
+  return (((size_t)slot * 2 + x) * (D / 4 + 1) + c4) * kT;
+}
+
+// Lanes 4k .. 4k + 3 hold four 16-byte pieces each of their rows: afterwards lane 4k + i holds piece i of the four rows.
+__device__ __forceinline__ void transpose_pieces(uint32_t (&w)[4][4], int lane) {
+#pragma unroll
+  for (int bit = 1; bit < 4; bit *= 2) {
+    const bool up = lane & bit;
+#pragma unroll
+    for (int a = 0; a < 4; ++a) {
+      if (a & bit) continue;
+      const int b = a | bit;
+#pragma unroll
+      for (int z = 0; z < 4; ++z) {
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? w[a][z] : w[b][z], bit);
+        if (up)
+          w[a][z] = got;
+        else
+          w[b][z] = got;
+      }
+    }
+  }
 }
 
 }  // namespace chunk
@@ -839,7 +869,12 @@ do {                                                                            
       if (ok) {
         const size_t out = (size_t)(g.tok + x * per_tile + tok) * in.heads + g.h * in.g + r % in.g;
         const float inv = l > 0.f ? 1.f / l : 0.f;
-        float* part = in.partial + ((size_t)g.slot * 2 * kT + x * kT + r) * kPartial<D>;
+        float4* part = reinterpret_cast<float4*>(in.partial) + partial_at<D>(g.slot, x, 0) + r;
+        // four lanes write one row's 64 bytes together: rows of the lanes whose pieces this one writes (or -1)
+        int to[4];  // (a call has fewer than 2^31 rows)
+#pragma unroll
+        for (int z = 0; z < 4; ++z)
+          to[z] = __shfl_sync(0xffffffffu, live ? (int)out : -1, (lane & ~3) + z);
 #pragma unroll
         for (int j = 0; j < D / 32; ++j) {
           uint32_t o[32];
@@ -850,32 +885,33 @@ do {                                                                            
 #pragma unroll
             for (int i = 0; i < 32; ++i) o[i] = 0u;
           }
-          if (live) {
-            if (g.slot < 0) {
-              uint4* dst = reinterpret_cast<uint4*>(in.o + out * D + j * 32);
+          if (g.slot < 0) {
+            uint32_t w[4][4];
 #pragma unroll
-              for (int i = 0; i < 32; i += 8) {
-                uint32_t w[4];
+            for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int z = 0; z < 4; ++z)
-                  w[z] = pack_bf16((__uint_as_float(o[i + 2 * z]) + vsum) * inv,
-                                   (__uint_as_float(o[i + 2 * z + 1]) + vsum) * inv);
-                dst[i / 8] = make_uint4(w[0], w[1], w[2], w[3]);
-              }
-            } else {
-              float4* dst = reinterpret_cast<float4*>(part + j * 32);
+              for (int z = 0; z < 4; ++z)
+                w[i][z] = pack_bf16((__uint_as_float(o[8 * i + 2 * z]) + vsum) * inv,
+                                    (__uint_as_float(o[8 * i + 2 * z + 1]) + vsum) * inv);
+            transpose_pieces(w, lane);
 #pragma unroll
-              for (int i = 0; i < 32; i += 4)
-                dst[i / 4] = make_float4(__uint_as_float(o[i]) + vsum, __uint_as_float(o[i + 1]) + vsum,
-                                         __uint_as_float(o[i + 2]) + vsum, __uint_as_float(o[i + 3]) + vsum);
-            }
+            for (int z = 0; z < 4; ++z)
+              if (to[z] >= 0)
+                *reinterpret_cast<uint4*>(in.o + (size_t)to[z] * D + j * 32 + 8 * (lane & 3)) =
+                    make_uint4(w[z][0], w[z][1], w[z][2], w[z][3]);
+          } else if (live) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              part[(j * 8 + i) * kT] =
+                  make_float4(__uint_as_float(o[4 * i]) + vsum, __uint_as_float(o[4 * i + 1]) + vsum,
+                              __uint_as_float(o[4 * i + 2]) + vsum, __uint_as_float(o[4 * i + 3]) + vsum);
           }
         }
         if (live) {
           if (g.slot < 0) {
             if (in.lse) in.lse[out] = l > 0.f ? (m_used + log2f(l)) * 0.69314718055994531f : -INFINITY;
           } else {
-            *reinterpret_cast<float4*>(part + D) = make_float4(m_used, l, l, 0.f);
+            part[(D / 4) * kT] = make_float4(m_used, l, l, 0.f);
           }
         }
         tc_fence_before();  // O has been read: ordered before the next unit's first P_FULL arrival
@@ -904,19 +940,105 @@ do {                                                                            
 // (i, y) stand for cut i + 1, and share the unit's rows with the blocks of its
 // other cuts.  What there is to join they read from the pieces' notes: finding
 // it again took each of the many blocks longer than the joining.
+// An item is 8 channels of 32 rows, a lane's one of them; with up to 8 pieces a warp takes an item, with more a CTA
+// does, its warps sharing the pieces.
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) s2_cache_chunk_join_kernel(const __grid_constant__ AttnIn in) {
   using namespace chunk;
-  __shared__ JoinShared<D> sh;
+  constexpr int kW = kJoinThreads / 32, kCols = D / 8;
+  __shared__ float4 sh_ml[kW][32], sh_o[kW][2][32];
   const int per_tile = kT / in.g;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   // every CTA waits, also one with nothing to do: the stream's next launch counts on this one's end alone
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  join_rows<D>(sh, static_cast<const JoinCut*>(in.cuts)[blockIdx.x], in.partial, 2 * kT, in.g, in.heads,
-               [&](int i) {
-                 const int tok = i / in.g;
-                 return (tok / per_tile) * kT + (tok % per_tile) * in.g + i % in.g;
-               },
-               in.o, in.lse);
+  const JoinCut u = static_cast<const JoinCut*>(in.cuts)[blockIdx.x];
+  if (u.rows == 0) return;
+  const int nth = u.nth * gridDim.y + blockIdx.y, helpers = u.helpers * gridDim.y;
+  const bool narrow = u.p1 - u.p0 < kJoinBatch;
+  for (int item = narrow ? nth * kW + warp : nth; item < 2 * (kT / 32) * kCols; item += narrow ? helpers * kW : helpers) {
+    const int rows = item / kCols, c4 = 2 * (item % kCols);
+    const int x = rows / (kT / 32), r0 = rows % (kT / 32) * 32, r = r0 + lane;
+    // row of the unit that row r of tile x is; they ascend, so where the first is none all are none
+    auto row_at = [&](int y) { return y < per_tile * in.g ? x * per_tile * in.g + y : INT_MAX; };
+    if (row_at(r0) >= u.rows) continue;
+    const int i = row_at(r);
+    const bool live = i < u.rows;
+    float m = -INFINITY, l = 0.f, div = 0.f;
+    float o[8];
+#pragma unroll
+    for (int z = 0; z < 8; ++z) o[z] = 0.f;
+    const int by = narrow ? 1 : kW;
+    for (int p = narrow ? u.p0 : u.p0 + warp; p <= u.p1; p += kJoinBatch * by) {
+      float4 ml[kJoinBatch], v[kJoinBatch][2];
+#pragma unroll
+      for (int k = 0; k < kJoinBatch; ++k) {
+        ml[k] = make_float4(-INFINITY, 0.f, 0.f, 0.f);
+        v[k][0] = v[k][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+        const int q = p + k * by;
+        if (live && q <= u.p1) {
+          const float4* from =
+              reinterpret_cast<const float4*>(in.partial) + partial_at<D>(2 * q + (q == u.begin), x, 0) + r;
+          ml[k] = from[(D / 4) * kT];
+          v[k][0] = from[c4 * kT];
+          v[k][1] = from[(c4 + 1) * kT];
+        }
+      }
+      float top = m;
+#pragma unroll
+      for (int k = 0; k < kJoinBatch; ++k) top = fmaxf(top, ml[k].x);
+      if (top == -INFINITY) continue;
+      const float f = ex2(m - top);
+      l *= f;
+      div *= f;
+#pragma unroll
+      for (int z = 0; z < 8; ++z) o[z] *= f;
+#pragma unroll
+      for (int k = 0; k < kJoinBatch; ++k) {
+        const float e = ex2(ml[k].x - top);
+        l = fmaf(ml[k].y, e, l);
+        div = fmaf(ml[k].z, e, div);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          o[4 * h] = fmaf(v[k][h].x, e, o[4 * h]), o[4 * h + 1] = fmaf(v[k][h].y, e, o[4 * h + 1]);
+          o[4 * h + 2] = fmaf(v[k][h].z, e, o[4 * h + 2]), o[4 * h + 3] = fmaf(v[k][h].w, e, o[4 * h + 3]);
+        }
+      }
+      m = top;
+    }
+    if (!narrow) {
+      __syncthreads();
+      sh_ml[warp][lane] = make_float4(m, l, div, 0.f);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) sh_o[warp][h][lane] = make_float4(o[4 * h], o[4 * h + 1], o[4 * h + 2], o[4 * h + 3]);
+      __syncthreads();
+      if (warp != 0) continue;
+#pragma unroll
+      for (int w = 1; w < kW; ++w) m = fmaxf(m, sh_ml[w][lane].x);
+      l = div = 0.f;
+#pragma unroll
+      for (int z = 0; z < 8; ++z) o[z] = 0.f;
+#pragma unroll
+      for (int w = 0; w < kW; ++w) {
+        const float4 t = sh_ml[w][lane];
+        const float e = m == -INFINITY ? 0.f : ex2(t.x - m);
+        l = fmaf(t.y, e, l);
+        div = fmaf(t.z, e, div);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float4 y = sh_o[w][h][lane];
+          o[4 * h] = fmaf(y.x, e, o[4 * h]), o[4 * h + 1] = fmaf(y.y, e, o[4 * h + 1]);
+          o[4 * h + 2] = fmaf(y.z, e, o[4 * h + 2]), o[4 * h + 3] = fmaf(y.w, e, o[4 * h + 3]);
+        }
+      }
+    }
+    if (!live) continue;
+    const float inv = l > 0.f ? 1.f / div : 0.f;
+    const size_t out = (size_t)(u.tok + i / in.g) * in.heads + u.head + i % in.g;
+    *reinterpret_cast<uint4*>(in.o + out * D + 4 * c4) =
+        make_uint4(pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv),
+                   pack_bf16(o[4] * inv, o[5] * inv), pack_bf16(o[6] * inv, o[7] * inv));
+    if (in.lse && c4 == 0) in.lse[out] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+  }
 }
 
 template <int D, bool Q4>

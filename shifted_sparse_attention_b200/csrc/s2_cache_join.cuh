@@ -1,5 +1,6 @@
 // s2_cache_join.cuh -- adding up the partial sums of a unit of cached attention
-// that several CTAs computed (s2_cache_attn.cu, s2_cache_chunk.cu).
+// that several CTAs computed, one row behind the other (s2_cache_attn.cu;
+// s2_cache_chunk.cu lays them transposed, and has its own loop).
 //
 // A piece leaves for each row O (D floats, not divided), then its maximum
 // score, the sum of its weights and what O is to be divided by; in the order of
@@ -93,24 +94,22 @@ __device__ __forceinline__ void join_pieces(int p, int by, int p1, int row, Part
   }
 }
 
-// Rows of a cut unit, shared out over the CTAs of its cuts (gridDim.y for each).  row_of_slot(i): place of row i
-// among the rows of a slot.
-template <int D, typename RowOfSlot>
+// Rows of a cut unit, shared out over the CTAs of its cuts.
+template <int D>
 __device__ __forceinline__ void join_rows(JoinShared<D>& sh, const JoinCut u, const float* partial, int slot_rows,
-                                          int g, int heads, RowOfSlot row_of_slot, __nv_bfloat16* o_all, float* lse) {
+                                          int g, int heads, __nv_bfloat16* o_all, float* lse) {
   constexpr int kW = kJoinThreads / 32, kV = D / 32;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   if (u.rows == 0) return;
-  const int nth = u.nth * gridDim.y + blockIdx.y, helpers = u.helpers * gridDim.y;
+  const int nth = u.nth, helpers = u.helpers;
   const bool narrow = u.p1 - u.p0 < kJoinBatch;
   const int first = narrow ? nth * kW + warp : nth, by = narrow ? helpers * kW : helpers;
   auto part = [&](int p, int row) {
     return partial + ((size_t)(2 * p + (p == u.begin)) * slot_rows + row) * kPartial<D>;
   };
   for (int i = first; i < u.rows; i += by) {
-    const int row = row_of_slot(i);
     float m, l, div, o[kV];
-    join_pieces<D>(narrow ? u.p0 : u.p0 + warp, narrow ? 1 : kW, u.p1, row, part, m, l, div, o);
+    join_pieces<D>(narrow ? u.p0 : u.p0 + warp, narrow ? 1 : kW, u.p1, i, part, m, l, div, o);
     if (!narrow) {
       __syncthreads();
       if (lane == 0) sh.m[warp] = m, sh.l[warp] = l, sh.d[warp] = div;
