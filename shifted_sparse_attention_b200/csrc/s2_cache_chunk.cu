@@ -157,9 +157,11 @@ __device__ __forceinline__ int pair_tiles(const Seq& s, const Units& u, int j) {
   const int first = j * u.d;
   return last_tile(s.len - s.n + first, min(u.d, s.n - first)) + 1;
 }
-// Key tiles of a unit that lie before point w of its weight (the same for all that ask, and growing with w).
+// Key tiles of a unit that lie before point w of its weight (the same for all that ask, and growing with w).  Where in
+// the unit a cut falls need not be exact: 32 bits are off by 2^-22 of the unit at most, far less than a piece.
 __device__ __forceinline__ int tile_at(int tiles, long long w, long long weight) {
-  return w >= weight ? tiles : min(tiles, __double2int_rd(__ddiv_rn((double)w * tiles, (double)weight)));
+  if (w >= weight) return tiles;
+  return min(tiles, __float2int_rd(__fdiv_rn(__fmul_rn((float)(int)w, (float)tiles), (float)(int)weight)));
 }
 
 // The next segments of a CTA's piece (one thread); returns their number.  What the piece's end cuts goes to `cut`.
@@ -942,10 +944,12 @@ do {                                                                            
 // it again took each of the many blocks longer than the joining.
 // An item is 8 channels of 32 rows, a lane's one of them; with up to 8 pieces a warp takes an item, with more a CTA
 // does, its warps sharing the pieces.
+// (Six CTAs to a cut, three on an SM, with four pieces' loads in flight: 60 tokens over 8000 keys 33 us; eight, one on an
+// SM, eight pieces: 41.)
 template <int D>
-__global__ void __launch_bounds__(kJoinThreads) s2_cache_chunk_join_kernel(const __grid_constant__ AttnIn in) {
+__global__ void __launch_bounds__(kJoinThreads, 3) s2_cache_chunk_join_kernel(const __grid_constant__ AttnIn in) {
   using namespace chunk;
-  constexpr int kW = kJoinThreads / 32, kCols = D / 8;
+  constexpr int kW = kJoinThreads / 32, kCols = D / 8, kBatch = 4;
   __shared__ float4 sh_ml[kW][32], sh_o[kW][2][32];
   const int per_tile = kT / in.g;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -968,10 +972,10 @@ __global__ void __launch_bounds__(kJoinThreads) s2_cache_chunk_join_kernel(const
 #pragma unroll
     for (int z = 0; z < 8; ++z) o[z] = 0.f;
     const int by = narrow ? 1 : kW;
-    for (int p = narrow ? u.p0 : u.p0 + warp; p <= u.p1; p += kJoinBatch * by) {
-      float4 ml[kJoinBatch], v[kJoinBatch][2];
+    for (int p = narrow ? u.p0 : u.p0 + warp; p <= u.p1; p += kBatch * by) {
+      float4 ml[kBatch], v[kBatch][2];
 #pragma unroll
-      for (int k = 0; k < kJoinBatch; ++k) {
+      for (int k = 0; k < kBatch; ++k) {
         ml[k] = make_float4(-INFINITY, 0.f, 0.f, 0.f);
         v[k][0] = v[k][1] = make_float4(0.f, 0.f, 0.f, 0.f);
         const int q = p + k * by;
@@ -985,7 +989,7 @@ __global__ void __launch_bounds__(kJoinThreads) s2_cache_chunk_join_kernel(const
       }
       float top = m;
 #pragma unroll
-      for (int k = 0; k < kJoinBatch; ++k) top = fmaxf(top, ml[k].x);
+      for (int k = 0; k < kBatch; ++k) top = fmaxf(top, ml[k].x);
       if (top == -INFINITY) continue;
       const float f = ex2(m - top);
       l *= f;
@@ -993,7 +997,7 @@ __global__ void __launch_bounds__(kJoinThreads) s2_cache_chunk_join_kernel(const
 #pragma unroll
       for (int z = 0; z < 8; ++z) o[z] *= f;
 #pragma unroll
-      for (int k = 0; k < kJoinBatch; ++k) {
+      for (int k = 0; k < kBatch; ++k) {
         const float e = ex2(ml[k].x - top);
         l = fmaf(ml[k].y, e, l);
         div = fmaf(ml[k].z, e, div);
@@ -1053,7 +1057,7 @@ static int chunk_impl(const CUtensorMap* tq, const CUtensorMap* tk, const CUtens
   e = cudaGetLastError();
   if (e != cudaSuccess) return (int)e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(in.pieces - 1, 8);
+  cfg.gridDim = dim3(in.pieces - 1, 6);
   cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = stream;
   cudaLaunchAttribute at[1];
