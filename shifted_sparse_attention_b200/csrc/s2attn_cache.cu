@@ -98,16 +98,20 @@ int64_t shared_rows(const s2_cache* cache, const s2_cache_batch* batch, int64_t 
   return n * (heads / cache->heads);
 }
 
-// Whether the call's bytes bound it (s2_cache_attn.cu: a key is read, and unpacked, once for every 16 query rows) or
-// its products (s2_cache_chunk.cu: 128 rows at a time, at 15 to 40 us for the first tiles).  One block of rows is the
-// former's always.  Beyond, keys times key/value heads times blocks of rows decide; us of one and the other, rows of
-// 128 channels: bf16 1 x 60 tokens over 8000 keys, 8 heads (9.7·10^5) 62 and 52, 4 x 150 over 1000, 2 heads (6.9·10^5)
-// 53 and 49, 1 x 400 over 1000, 2 heads (5.6·10^5) 41 and 45; 4 bits 4 x 400 over 1000, 8 heads (4.5·10^6) 230 and 106,
-// 1 x 150 over 8000, 2 heads (1.2·10^6) 60 and 66.
+// Which kernel: s2_cache_attn.cu reads (and unpacks) a key once for every 16 query rows and starts quickly,
+// s2_cache_chunk.cu once for every 128 and takes 14 us longer to start and end, 17 from 4 bits.  Keys that both go over,
+// with what a block of rows costs beside them, decide: the measured times are 8 + 6.5e-5 and 22 + 7e-5 us for each of
+// them in bf16, 9 + 4.5e-5 and 26 + 1e-4 in 4 bits, about half of that for half the channels.  us of one and the
+// other (tokens over keys, key/value heads; 4 query heads to each, bf16 / 4 bits): 60 over 8000, 8 heads 61 / 49 and 34 /
+// 39; 512 over 512 52 / 47 and 28 / 32; 256 over 256 20 / 19 and 27 / 30; 60 over 2000 25 / 23 and 28 / 32; 16 sequences of
+// 5 over 2000 42 / 35 and 45 / 57.
 bool few_rows(const s2_cache* cache, const s2_cache_batch* batch, int64_t heads) {
-  const int64_t rows = shared_rows(cache, batch, heads), len = batch->max_len ? batch->max_len : batch->table_width * cache->page_size;
-  const double work = (double)batch->seqs * (double)len * (double)cache->heads * (double)((rows + 15) / 16);
-  return rows <= 16 || work <= (cache->format == S2_CACHE_Q4 ? 1e6 : 7e5);
+  const bool q4 = cache->format == S2_CACHE_Q4;
+  const double rows = (double)shared_rows(cache, batch, heads), units = (double)batch->seqs * (double)cache->heads;
+  const double len = (double)(batch->max_len ? batch->max_len : batch->table_width * cache->page_size);
+  const double few = units * std::ceil(rows / 16) * (len + (q4 ? 256 : 128));
+  const double many = units * std::ceil(rows / 128) * (len + 256);
+  return (few - (q4 ? 2.2 : 1.0) * many) * ((double)cache->D / 128) <= (q4 ? 4e5 : 2.5e5);
 }
 
 int launched(int rc, const char* what) {
