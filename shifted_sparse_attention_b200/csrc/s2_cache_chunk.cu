@@ -27,11 +27,12 @@
 // scale and min of each key: s = sk (q·k') + (mk - 128 sk) sum(q); the weight that
 // goes into the product is p·sv (rounded to bf16, relative 2^-9), and
 // sum p (mv + 8 sv), the same for every channel, is kept beside O.
-// Measured: 2048 tokens (32 heads, 8 key heads, D 128) over 16384 keys 457 us,
-// 1128 TFLOP/s (the products alone would take 312): the softmax's hand-off
+// Measured: 2048 tokens (32 heads, 8 key heads, D 128) over 16384 keys 435
+// to 446 us, 1170 TFLOP/s (the products alone would take 312): the softmax's hand-off
 // chain bounds it (tensor pipe 56%).  4 bits, three chunks of 260 to 1000
-// tokens over 3000 to 12000 keys 353 us; as bf16 pages 245: the difference is
-// the softmax's work on each key's scale and min.
+// tokens over 3000 to 12000 keys 333 us, bound by the softmax's work on each
+// key's scale and min.  Short calls: 60 tokens over 8000 keys 33 us, of which
+// finding the first segment takes 4, loading 2, the sums' way out 3, the join 10.
 #include <climits>
 
 #include <cuda.h>
