@@ -684,6 +684,7 @@ do {                                                                            
       float vsum = 0.f, qsum = 0.f;
       if (Q4 && keys) {
         ok = s2_wait(bar(Q_FULL), n_seg & 1, abort_flag, status, 4);
+        ok = __all_sync(0xffffffffu, ok);  // a warp gives up together: what follows needs all of its lanes
         ++n_seg;
         if (ok && has && live) {
           for (int i = 0; i < 8 * kChunks; ++i) {
@@ -705,6 +706,7 @@ do {                                                                            
           if constexpr (Q4) {
             // the other tile's keys: only counted
             ok = s2_wait(bar(SC_FULL + sc), (n_sc / kScaleSlots) & 1, abort_flag, status, 4);
+            ok = __all_sync(0xffffffffu, ok);
             if (ok) mbar_arrive(bar(SC_EMPTY + sc));
             ++n_sc;
             continue;
@@ -716,6 +718,7 @@ do {                                                                            
         if constexpr (Q4) {
           if (ok) ok = s2_wait(bar(SC_FULL + sc), (n_sc / kScaleSlots) & 1, abort_flag, status, 4);
         }
+        ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
         ++nS;
@@ -865,6 +868,7 @@ do {                                                                            
       }
       if (ok && has) {
         ok = s2_wait(bar(O_FULL + x), nO & 1, abort_flag, status, 4);
+        ok = __all_sync(0xffffffffu, ok);
         ++nO;
         tc_fence_after();
       }
