@@ -97,9 +97,11 @@ __device__ __forceinline__ float4 ld_cluster16(const void* p, int rank) {
                : "memory");
   return v;
 }
-// All threads of all of the cluster's CTAs; what they wrote before is seen by all after.
+// All threads of all of the cluster's CTAs; what they wrote before is seen by all after.  Not the .aligned form: that one
+// wants a warp's lanes together, and they come from loops that end at different turns (a row of 64 channels is half a
+// warp's) and from stores that one lane in 16 or 32 makes.
 __device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.arrive;\n\tbarrier.cluster.wait;" ::: "memory");
 }
 
 // Registers of one 16-key block of K and of V in the order the products take them.

@@ -546,3 +546,14 @@ def test_packing_of_rows_wider_than_32_bits():
     s2.cache_append(cache, batch, x.cuda(), x.cuda(), base=0.0)
     for t in s2.cache_read(cache, batch):
         assert torch.isnan(t[0]).all() and torch.isfinite(t[1]).all()
+
+
+@pytest.mark.parametrize("bits", [16, 4])
+@pytest.mark.parametrize("H,Hkv,lens,news", [
+    (3, 1, [700], [1]), (1, 1, [513], [1]), (5, 1, [1000, 40], [1, 3]), (7, 1, [900, 0, 333], [1, 1, 1]),
+])
+def test_clusters_whose_rows_end_inside_a_warp(bits, H, Hkv, lens, news):
+    # rows of 64 channels are half a warp's work: an odd number of them ends the last turn of a warp's lanes apart, and
+    # the lanes that write lse part as well, right before the cluster's CTAs meet
+    c = ref.Paged(lens, Hkv, 64, 16, bits, seed=H)
+    check_attention(c, news, H, max_new=max(news), max_len=max(lens))
