@@ -498,8 +498,7 @@ __global__ void __launch_bounds__(W * 32, ctas_per_sm<Q4, NR, W>())
               float w[2];
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
-                const float base = m[y][e] == -INFINITY ? 0.f : m[y][e];
-                w[e] = ex2(fmaf(s[y][u][2 * t + e], in.scale_log2, -base));
+                w[e] = ex2(fmaf(s[y][u][2 * t + e], in.scale_log2, -base_of(m[y][e])));
                 l[y][e] += w[e];
               }
               if constexpr (Q4) {
@@ -597,8 +596,8 @@ __global__ void __launch_bounds__(W * 32, ctas_per_sm<Q4, NR, W>())
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < W; ++w) {
-        if (sh.m[w][row] == -INFINITY) continue;
-        const float f = ex2(sh.m[w][row] - mm);
+        if (sh.l[w][row] == 0.f) continue;  // saw no key
+        const float f = ex2(sh.m[w][row] - base_of(mm));
         const float4 v = *reinterpret_cast<const float4*>(&sh.o[w][row][d]);
         ll += sh.l[w][row] * f;
         div += sh.div[w][row] * f;
@@ -610,10 +609,10 @@ __global__ void __launch_bounds__(W * 32, ctas_per_sm<Q4, NR, W>())
       } else if (slot < 0) {
         const int at = rb * kRows + row;
         const size_t out = (size_t)(seq.first + at / in.g) * in.heads + h * in.g + at % in.g;
-        const float inv = ll > 0.f ? 1.f / div : 0.f;
+        const float inv = row_scale(ll, div);
         *reinterpret_cast<uint2*>(in.o + out * D + d) =
             make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
-        if (in.lse && d == 0) in.lse[out] = ll > 0.f ? (mm + log2f(ll)) * 0.69314718055994531f : -INFINITY;
+        if (in.lse && d == 0) in.lse[out] = row_lse(mm, ll);
       } else {
         *reinterpret_cast<float4*>(part + row * kPartial<D> + d) = o;
         if (d == 0) *reinterpret_cast<float4*>(part + row * kPartial<D> + D) = make_float4(mm, ll, div, 0.f);
@@ -638,7 +637,7 @@ __global__ void __launch_bounds__(W * 32, ctas_per_sm<Q4, NR, W>())
         for (int p = 0; p < kMaxCluster; ++p) mm = fmaxf(mm, ml[p].x);
 #pragma unroll
         for (int p = 0; p < kMaxCluster; ++p) {
-          const float f = ml[p].x == -INFINITY ? 0.f : ex2(ml[p].x - mm);
+          const float f = ex2(ml[p].x - base_of(mm));
           ll = fmaf(ml[p].y, f, ll);
           div = fmaf(ml[p].z, f, div);
           o.x = fmaf(v[p].x, f, o.x), o.y = fmaf(v[p].y, f, o.y);
@@ -646,10 +645,10 @@ __global__ void __launch_bounds__(W * 32, ctas_per_sm<Q4, NR, W>())
         }
         const int at = rb * kRows + row;
         const size_t out = (size_t)(seq.first + at / in.g) * in.heads + h * in.g + at % in.g;
-        const float inv = ll > 0.f ? 1.f / div : 0.f;
+        const float inv = row_scale(ll, div);
         *reinterpret_cast<uint2*>(in.o + out * D + d) =
             make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
-        if (in.lse && d == 0) in.lse[out] = ll > 0.f ? (mm + log2f(ll)) * 0.69314718055994531f : -INFINITY;
+        if (in.lse && d == 0) in.lse[out] = row_lse(mm, ll);
       }
       cluster_sync();  // nobody leaves while its sums are being read
     }

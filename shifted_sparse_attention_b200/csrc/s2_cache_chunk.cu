@@ -783,7 +783,7 @@ do {                                                                            
                 w[i] = pack_bf16(__uint_as_float(w[i] << 16) * f, __uint_as_float(w[i] & 0xffff0000u) * f);
               tmem_st32(tS, w);
             }
-            const float m_exp = (m_used == -INFINITY) ? 0.f : m_used;
+            const float m_exp = base_of(m_used);
             const float2 nm2 = make_float2(-m_exp, -m_exp);
             float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)}, vacc = make_float2(0.f, 0.f);
             uint32_t pk[32];
@@ -834,7 +834,7 @@ do {                                                                            
             l *= factor;
             m_used = m_new;
           }
-          const float m_exp = (m_used == -INFINITY) ? 0.f : m_used;
+          const float m_exp = base_of(m_used);
           const float2 nm2 = make_float2(-m_exp, -m_exp);
           float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
@@ -875,7 +875,7 @@ do {                                                                            
       // ------------------------------------------------------ rows out
       if (ok) {
         const size_t out = (size_t)(g.tok + x * per_tile + tok) * in.heads + g.h * in.g + r % in.g;
-        const float inv = l > 0.f ? 1.f / l : 0.f;
+        const float inv = row_scale(l, l);
         float4* part = reinterpret_cast<float4*>(in.partial) + partial_at<D>(g.slot, x, 0) + r;
         // four lanes write one row's 64 bytes together: rows of the lanes whose pieces this one writes (or -1)
         int to[4];  // (a call has fewer than 2^31 rows)
@@ -916,7 +916,7 @@ do {                                                                            
         }
         if (live) {
           if (g.slot < 0) {
-            if (in.lse) in.lse[out] = l > 0.f ? (m_used + log2f(l)) * 0.69314718055994531f : -INFINITY;
+            if (in.lse) in.lse[out] = row_lse(m_used, l);
           } else {
             part[(D / 4) * kT] = make_float4(m_used, l, l, 0.f);
           }
@@ -995,15 +995,16 @@ __global__ void __launch_bounds__(kJoinThreads, 3) s2_cache_chunk_join_kernel(co
       float top = m;
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) top = fmaxf(top, ml[k].x);
-      if (top == -INFINITY) continue;
-      const float f = ex2(m - top);
+      const float base = base_of(top), f = ex2(m - base);
       l *= f;
       div *= f;
 #pragma unroll
       for (int z = 0; z < 8; ++z) o[z] *= f;
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
-        const float e = ex2(ml[k].x - top);
+        const float e = ex2(ml[k].x - base);
+        // a piece in which the row sees no key adds nothing, even where its weights of 0 met values that are not finite
+        if (ml[k].y == 0.f) v[k][0] = v[k][1] = make_float4(0.f, 0.f, 0.f, 0.f);
         l = fmaf(ml[k].y, e, l);
         div = fmaf(ml[k].z, e, div);
 #pragma unroll
@@ -1029,7 +1030,7 @@ __global__ void __launch_bounds__(kJoinThreads, 3) s2_cache_chunk_join_kernel(co
 #pragma unroll
       for (int w = 0; w < kW; ++w) {
         const float4 t = sh_ml[w][lane];
-        const float e = m == -INFINITY ? 0.f : ex2(t.x - m);
+        const float e = ex2(t.x - base_of(m));
         l = fmaf(t.y, e, l);
         div = fmaf(t.z, e, div);
 #pragma unroll
@@ -1041,12 +1042,12 @@ __global__ void __launch_bounds__(kJoinThreads, 3) s2_cache_chunk_join_kernel(co
       }
     }
     if (!live) continue;
-    const float inv = l > 0.f ? 1.f / div : 0.f;
+    const float inv = row_scale(l, div);
     const size_t out = (size_t)(u.tok + i / in.g) * in.heads + u.head + i % in.g;
     *reinterpret_cast<uint4*>(in.o + out * D + 4 * c4) =
         make_uint4(pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv),
                    pack_bf16(o[4] * inv, o[5] * inv), pack_bf16(o[6] * inv, o[7] * inv));
-    if (in.lse && c4 == 0) in.lse[out] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+    if (in.lse && c4 == 0) in.lse[out] = row_lse(m, l);
   }
 }
 

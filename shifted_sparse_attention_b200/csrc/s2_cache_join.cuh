@@ -7,6 +7,8 @@
 // the pieces
 //     m = max m_p,  o = sum 2^(m_p - m) O_p / sum 2^(m_p - m) d_p,
 // and lse from the sum of weights.
+// A row has seen no key exactly where its sum of weights is 0.  Its maximum does not tell: a maximum leaves NaN out, so
+// that of NaN scores alone is -inf too, while their sum is NaN and has to come through.
 // What bounds it is the latency of reading them, so all of a warp's loads are
 // asked for before the first is used: with up to 8 pieces a warp takes a row,
 // with more a CTA does, its warps sharing the pieces.
@@ -17,6 +19,12 @@
 #include "sm100_ptx.cuh"
 
 namespace s2 {
+
+// What a row's maximum is taken from scores as: 0 where there is none, so that no -inf - (-inf) arises.
+__device__ __forceinline__ float base_of(float m) { return m == -INFINITY ? 0.f : m; }
+// 1 / d of a row whose weights' sum is l, 0 for a row without keys; and its lse (natural logarithm), -inf without keys.
+__device__ __forceinline__ float row_scale(float l, float d) { return l == 0.f ? 0.f : 1.f / d; }
+__device__ __forceinline__ float row_lse(float m, float l) { return (m + log2f(l)) * 0.69314718055994531f; }
 
 constexpr int kJoinThreads = 256;
 constexpr int kJoinBatch = 8;  // pieces that a warp asks for at once
@@ -76,15 +84,14 @@ __device__ __forceinline__ void join_pieces(int p, int by, int p1, int row, Part
     float top = m;
 #pragma unroll
     for (int i = 0; i < kJoinBatch; ++i) top = fmaxf(top, ml[i].x);
-    if (top == -INFINITY) continue;
-    const float f = ex2(m - top);
+    const float base = base_of(top), f = ex2(m - base);
     l *= f;
     d *= f;
 #pragma unroll
     for (int z = 0; z < kV; ++z) o[z] *= f;
 #pragma unroll
     for (int i = 0; i < kJoinBatch; ++i) {
-      const float g = ex2(ml[i].x - top);
+      const float g = ex2(ml[i].x - base);
       l = fmaf(ml[i].y, g, l);
       d = fmaf(ml[i].z, g, d);
 #pragma unroll
@@ -124,14 +131,14 @@ __device__ __forceinline__ void join_rows(JoinShared<D>& sh, const JoinCut u, co
       for (int z = 0; z < kV; ++z) o[z] = 0.f;
 #pragma unroll
       for (int w = 0; w < kW; ++w) {
-        const float f = m == -INFINITY ? 0.f : ex2(sh.m[w] - m);
+        const float f = ex2(sh.m[w] - base_of(m));
         l = fmaf(sh.l[w], f, l);
         div = fmaf(sh.d[w], f, div);
 #pragma unroll
         for (int z = 0; z < kV; ++z) o[z] = fmaf(sh.o[w][kV * lane + z], f, o[z]);
       }
     }
-    const float inv = l > 0.f ? 1.f / div : 0.f;
+    const float inv = row_scale(l, div);
     const int at = u.row0 + i;
     const size_t out = (size_t)(u.tok + at / g) * heads + u.head + at % g;
     uint32_t* dst = reinterpret_cast<uint32_t*>(o_all + out * D) + lane * (kV / 2);
@@ -139,7 +146,7 @@ __device__ __forceinline__ void join_rows(JoinShared<D>& sh, const JoinCut u, co
       *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv));
     else
       *dst = pack_bf16(o[0] * inv, o[1] * inv);
-    if (lse && lane == 0) lse[out] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+    if (lse && lane == 0) lse[out] = row_lse(m, l);
   }
 }
 

@@ -557,3 +557,65 @@ def test_clusters_whose_rows_end_inside_a_warp(bits, H, Hkv, lens, news):
     # the lanes that write lse part as well, right before the cluster's CTAs meet
     c = ref.Paged(lens, Hkv, 64, 16, bits, seed=H)
     check_attention(c, news, H, max_new=max(news), max_len=max(lens))
+
+
+def check_not_finite(c, news, H, q, **kw):
+    """As check_attention for queries and keys that hold NaN or infinities: o and lse are NaN and infinite where the
+    definition's are, and near it elsewhere.  Returns o, lse and the definition's."""
+    T, wide = sum(news), kw.pop("wide", False)
+    o, lse, to, tl = ref.attention(c, q, starts_of(news))
+    got_lse = torch.empty(T, H, device="cuda")
+    got = s2.cache_attention(on_gpu(c), batch_of(c, news, wide=wide, **kw), q.cuda(), lse=got_lse)
+    s2.check_status()
+    got, got_lse = got.double().cpu(), got_lse.double().cpu()
+    assert torch.equal(got.isnan(), o.isnan())
+    assert torch.equal(got_lse.isnan(), lse.isnan())
+    assert torch.equal(got_lse.nan_to_num(0, 1, -1).where(got_lse.isinf(), 0.0), lse.nan_to_num(0, 1, -1).where(lse.isinf(), 0.0))
+    some = o.isfinite()
+    assert ((got - o).abs() <= to)[some].all()
+    some = lse.isfinite()
+    assert ((got_lse - lse).abs() <= tl)[some].all()
+    return got, got_lse, o, lse
+
+
+# units taken whole by one CTA or by a cluster, cut over CTAs, and the kernel for many rows (whole and cut)
+PATHS = ["whole", "cut", "many"]
+
+
+def hints_of(path, lens, news):
+    return {"whole": dict(max_new=max(news), max_len=min(max(lens), 512)), "cut": dict(max_new=max(news)),
+            "many": dict(max_new=max(news), wide=True)}[path]
+
+
+@pytest.mark.parametrize("path", PATHS)
+@pytest.mark.parametrize("bits", [16, 4])
+@pytest.mark.parametrize("lens,news", [([1], [1]), ([16], [1]), ([17], [1]), ([33], [1]), ([513], [1]), ([40, 9001], [3, 5]),
+                                       ([129], [2]), ([9000], [300])])
+def test_a_query_that_holds_nan(bits, lens, news, path):
+    c = ref.Paged(lens, 2, 128, 16, bits, seed=lens[0])
+    T, H = sum(news), 48 if path == "many" else 6
+    q = torch.randn(T, H, 128, generator=torch.Generator().manual_seed(T)).bfloat16()
+    q[T - 1, H - 2, 77] = float("nan")  # one row, on the second key head
+    got, _, _, _ = check_not_finite(c, news, H, q, **hints_of(path, lens, news))
+    assert got[T - 1, H - 2].isnan().all() and got.isnan().sum() == 128
+
+
+@pytest.mark.parametrize("path", PATHS)
+@pytest.mark.parametrize("bits", [16, 4])
+@pytest.mark.parametrize("lens,news,at", [  # the newest key alone in its step, tile or piece; and one far from both ends
+    ([1], [1], 0), ([16], [1], 15), ([17], [1], 16), ([33], [1], 32), ([513], [1], 512), ([129], [1], 128),
+    ([300], [40], 290), ([9001], [3], 9000), ([9000], [300], 8999), ([9000], [300], 4321), ([9000], [300], 0),
+])
+def test_a_key_that_holds_nan(bits, lens, news, at, path):
+    # a 4-bit row is NaN as append leaves a broken one
+    c = ref.Paged(lens, 2, 128, 16, bits, seed=lens[0])
+    page = int(c.table[0, at // 16])
+    if bits == 16:
+        c.k[page, 1, at % 16, 5] = float("nan")
+    else:
+        c.ks[page, 1, at % 16] = float("nan")
+    H = 48 if path == "many" else 4
+    q = torch.randn(sum(news), H, 128, generator=torch.Generator().manual_seed(at)).bfloat16()
+    got, _, _, _ = check_not_finite(c, news, H, q, **hints_of(path, lens, news))
+    seen = lens[0] - news[0] + torch.arange(news[0]) >= at
+    assert got[seen][:, H // 2:].isnan().all() and got[:, :H // 2].isfinite().all()
