@@ -479,7 +479,7 @@ __global__ void __launch_bounds__(W * 32, ctas_per_sm<Q4, NR, W>())
 #pragma unroll
               for (int off = 4; off < 32; off <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, off));
               t = fmaxf(t, m[y][e]);
-              const float f = t == -INFINITY ? 1.f : ex2(m[y][e] - t);
+              const float f = t == m[y][e] ? 1.f : ex2(m[y][e] - t);
               m[y][e] = t;
               l[y][e] *= f;
               vsum[y][e] *= f;
@@ -609,7 +609,7 @@ __global__ void __launch_bounds__(W * 32, ctas_per_sm<Q4, NR, W>())
       } else if (slot < 0) {
         const int at = rb * kRows + row;
         const size_t out = (size_t)(seq.first + at / in.g) * in.heads + h * in.g + at % in.g;
-        const float inv = row_scale(ll, div);
+        const float inv = row_scale(ll, div, seq.len - seq.n + at / in.g);
         *reinterpret_cast<uint2*>(in.o + out * D + d) =
             make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
         if (in.lse && d == 0) in.lse[out] = row_lse(mm, ll);
@@ -645,7 +645,7 @@ __global__ void __launch_bounds__(W * 32, ctas_per_sm<Q4, NR, W>())
         }
         const int at = rb * kRows + row;
         const size_t out = (size_t)(seq.first + at / in.g) * in.heads + h * in.g + at % in.g;
-        const float inv = row_scale(ll, div);
+        const float inv = row_scale(ll, div, seq.len - seq.n + at / in.g);
         *reinterpret_cast<uint2*>(in.o + out * D + d) =
             make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
         if (in.lse && d == 0) in.lse[out] = row_lse(mm, ll);
@@ -686,6 +686,7 @@ __global__ void __launch_bounds__(kJoinThreads) s2_cache_join_kernel(const __gri
       u.nth = (int)blockIdx.x - u.p0;
       u.helpers = u.p1 - u.p0;
       u.tok = seq.first;
+      u.place = seq.len - seq.n;
       u.row0 = rb * kRows;
       u.head = h * in.g;
     }

@@ -212,6 +212,7 @@ __device__ __noinline__ int walk_on(Walk& w, const CacheArgs& c, int g_heads, in
       u.p0 = p0 + (tile_at(tiles, w.piece * (p0 + 1) - begin, weight) == 0);
       u.p1 = p1 - (tile_at(tiles, w.piece * p1 - begin, weight) == tiles);
       u.tok = s.first + w.j * u_d;
+      u.place = s.len - s.n + w.j * u_d;
       u.row0 = 0;
       u.head = w.h * g_heads;
       if (u.p0 < u.p1) *cut = u;  // else one piece has all of the unit's tiles, and writes its rows
@@ -875,7 +876,7 @@ do {                                                                            
       // ------------------------------------------------------ rows out
       if (ok) {
         const size_t out = (size_t)(g.tok + x * per_tile + tok) * in.heads + g.h * in.g + r % in.g;
-        const float inv = row_scale(l, l);
+        const float inv = row_scale(l, l, place);
         float4* part = reinterpret_cast<float4*>(in.partial) + partial_at<D>(g.slot, x, 0) + r;
         // four lanes write one row's 64 bytes together: rows of the lanes whose pieces this one writes (or -1)
         int to[4];  // (a call has fewer than 2^31 rows)
@@ -1042,7 +1043,7 @@ __global__ void __launch_bounds__(kJoinThreads, 3) s2_cache_chunk_join_kernel(co
       }
     }
     if (!live) continue;
-    const float inv = row_scale(l, div);
+    const float inv = row_scale(l, div, u.place + i / in.g);
     const size_t out = (size_t)(u.tok + i / in.g) * in.heads + u.head + i % in.g;
     *reinterpret_cast<uint4*>(in.o + out * D + 4 * c4) =
         make_uint4(pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv),

@@ -20,10 +20,15 @@
 
 namespace s2 {
 
-// What a row's maximum is taken from scores as: 0 where there is none, so that no -inf - (-inf) arises.
-__device__ __forceinline__ float base_of(float m) { return m == -INFINITY ? 0.f : m; }
-// 1 / d of a row whose weights' sum is l, 0 for a row without keys; and its lse (natural logarithm), -inf without keys.
-__device__ __forceinline__ float row_scale(float l, float d) { return l == 0.f ? 0.f : 1.f / d; }
+// What scores are taken from for a maximum m: 0 where that is infinite, so that no infinity is taken from another (a
+// score of inf then has a weight of inf, and lse is inf as its definition says).
+__device__ __forceinline__ float base_of(float m) { return fabsf(m) == INFINITY ? 0.f : m; }
+// 1 / d of a row whose weights' sum is l.  l = 0: the token at `place` sees no key (place < 0) and gets 0, or its scores
+// are all -inf, and o is 0 / 0.
+__device__ __forceinline__ float row_scale(float l, float d, int place) {
+  return l != 0.f ? 1.f / d : place < 0 ? 0.f : NAN;
+}
+// lse in natural logarithms; -inf of a row without keys.
 __device__ __forceinline__ float row_lse(float m, float l) { return (m + log2f(l)) * 0.69314718055994531f; }
 
 constexpr int kJoinThreads = 256;
@@ -41,7 +46,8 @@ struct alignas(16) JoinCut {
   int p0, p1;        // pieces that hold sums
   int tok, row0;     // row i is query row row0 + i of the heads from `head` on, from token tok on
   int head;
-  int pad[3];
+  int place;         // of token tok
+  int pad[2];
 };
 constexpr size_t kCutBytes = 8192;  // of a workspace, before the sums, where pieces note what they cut
 
@@ -138,8 +144,8 @@ __device__ __forceinline__ void join_rows(JoinShared<D>& sh, const JoinCut u, co
         for (int z = 0; z < kV; ++z) o[z] = fmaf(sh.o[w][kV * lane + z], f, o[z]);
       }
     }
-    const float inv = row_scale(l, div);
     const int at = u.row0 + i;
+    const float inv = row_scale(l, div, u.place + at / g);
     const size_t out = (size_t)(u.tok + at / g) * heads + u.head + at % g;
     uint32_t* dst = reinterpret_cast<uint32_t*>(o_all + out * D) + lane * (kV / 2);
     if constexpr (kV == 4)

@@ -619,3 +619,37 @@ def test_a_key_that_holds_nan(bits, lens, news, at, path):
     got, _, _, _ = check_not_finite(c, news, H, q, **hints_of(path, lens, news))
     seen = lens[0] - news[0] + torch.arange(news[0]) >= at
     assert got[seen][:, H // 2:].isnan().all() and got[:, :H // 2].isfinite().all()
+
+
+@pytest.mark.parametrize("path", PATHS)
+@pytest.mark.parametrize("lens,news,at", [
+    ([1], [1], [0]), ([17], [1], [16]), ([17], [1], [3, 4, 16]), ([513], [1], [512]), ([300], [40], [290]),
+    ([9001], [3], [5000, 17]), ([9000], [300], [8900, 4321]), ([20], [1], range(20)), ([700], [300], range(700)),
+])
+def test_scores_that_are_infinite(lens, news, at, path):
+    """A key with an infinity meets queries of both signs in its channel: a score of inf makes lse inf and o NaN
+    (inf / inf), one of -inf has no weight, and where all are -inf, o is 0 / 0 and lse -inf."""
+    c = ref.Paged(lens, 2, 128, 16, 16, seed=lens[0])
+    H, T = 48 if path == "many" else 4, sum(news)
+    q = torch.randn(T, H, 128, generator=torch.Generator().manual_seed(at[0])).bfloat16()
+    q[:, ::2, 0], q[:, 1::2, 0] = 1.0, -1.0
+    # what the keys of score -inf leave: as if it were about -1000 / sqrt(128) = -88, a weight below 2^-100
+    for p in at:
+        c.k[int(c.table[0, p // 16]), 1, p % 16, 0] = 1000.0
+    o, lse, to, tl = ref.attention(c, q, starts_of(news))
+    for p in at:
+        c.k[int(c.table[0, p // 16]), 1, p % 16, 0] = float("inf")
+    hints = hints_of(path, lens, news)
+    got_lse = torch.empty(T, H, device="cuda")
+    got = s2.cache_attention(on_gpu(c), batch_of(c, news, wide=hints.pop("wide", False), **hints), q.cuda(), lse=got_lse)
+    s2.check_status()
+    got, got_lse = got.double().cpu(), got_lse.double().cpu()
+    place = lens[0] - news[0] + torch.arange(T)
+    on_second = torch.arange(H) >= H // 2
+    hit = (place >= min(at))[:, None] & on_second  # rows that see such a key
+    up, down = hit & (torch.arange(H) % 2 == 0), hit & (torch.arange(H) % 2 == 1)
+    none = down & torch.tensor([all(j in at for j in range(int(p) + 1)) for p in place])[:, None]  # and no other
+    assert got[up].isnan().all() and (got_lse[up] == float("inf")).all()
+    assert got[none].isnan().all() and (got_lse[none] == -float("inf")).all()
+    rest = ~up & ~none
+    assert ((got - o).abs() <= to)[rest].all() and ((got_lse - lse).abs() <= tl)[rest].all()
