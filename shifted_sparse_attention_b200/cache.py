@@ -221,7 +221,8 @@ def cache_read(cache: KVCache, batch: CacheBatch, out=None, stream=None):
 
 
 def cache_attention_workspace(cache: KVCache, batch: CacheBatch, heads: int):
-    """A workspace for cache_attention, to keep over steps.  Calls that may overlap on the GPU need one each."""
+    """A workspace for cache_attention, to keep over steps: it serves every batch and number of heads over caches of this
+    many channels.  Calls that may overlap on the GPU need one each."""
     n = s2attn_cache_attn_workspace_size(cache, batch, heads)
     if n == 0:
         raise ValueError("%d heads, this cache and this batch do not go together: %s" % (

@@ -183,8 +183,10 @@ int s2attn_cache_read(const s2_cache* cache, const s2_cache_batch* batch, void* 
 size_t s2attn_cache_attn_workspace_size(const s2_cache* cache, const s2_cache_batch* batch, int64_t heads) {
   s2::CacheArgs a;
   if (take(cache, batch, &a) != S2_OK || check_heads(cache, heads) != S2_OK) return 0;
-  return few_rows(cache, batch, heads) ? s2::cache_decode_partial_bytes((int)cache->D)
-                                       : s2::cache_chunk_partial_bytes((int)cache->D);
+  // of the kernel that needs more, whichever this batch takes: a program keeps its workspace while sequences come, grow
+  // and go, and with them the choice of the kernel changes
+  const size_t few = s2::cache_decode_partial_bytes((int)cache->D), many = s2::cache_chunk_partial_bytes((int)cache->D);
+  return few > many ? few : many;
 }
 
 int s2attn_cache_attn(const s2_cache* cache, const s2_cache_batch* batch, const void* q, int64_t ldq, void* o,

@@ -90,6 +90,24 @@ def test_attention_and_read_arguments(abi):
     assert L.s2attn_cache_read(pc, None, FAKE, FAKE, None) == -1
 
 
+@pytest.mark.parametrize("D,format", [(128, 0), (64, 0), (128, 1), (64, 1)])
+def test_one_workspace_serves_every_batch_of_a_cache(abi, D, format):
+    """What a program learns of its sequences as they grow (and how many take part, with how many tokens) chooses
+    kernels; the workspace that it keeps must do for all of them."""
+    L = abi.lib()
+    scales = dict(k_scale=FAKE, v_scale=FAKE) if format else {}
+    sizes = set()
+    for seqs, tokens, max_new in [(1, 1, 1), (16, 80, 5), (64, 64, 1), (3, 2000, 1000), (1, 2048, 2048), (9, 700, 0)]:
+        for width, max_len in [(4, 0), (1 << 12, 0), (1 << 12, 40), (1 << 12, 3800), (1 << 12, 3900), (1 << 12, 65536)]:
+            for heads in (2, 8, 32):
+                c, b = structs(D=D, format=format, seqs=seqs, tokens=tokens, max_new=max_new, table_width=width,
+                               max_len=max_len, **scales)
+                n = L.s2attn_cache_attn_workspace_size(ctypes.byref(c), ctypes.byref(b), heads)
+                assert n > 0
+                sizes.add(n)
+    assert len(sizes) == 1
+
+
 def test_tensor_helpers_refuse_host_tensors(abi):
     import shifted_sparse_attention_b200 as s2
     x = torch.zeros(2, 2, 16, 128, dtype=torch.bfloat16)

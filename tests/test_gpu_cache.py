@@ -653,3 +653,22 @@ def test_scores_that_are_infinite(lens, news, at, path):
     assert got[none].isnan().all() and (got_lse[none] == -float("inf")).all()
     rest = ~up & ~none
     assert ((got - o).abs() <= to)[rest].all() and ((got_lse - lse).abs() <= tl)[rest].all()
+
+
+@pytest.mark.parametrize("bits", [16, 4])
+def test_one_workspace_over_a_conversation(bits):
+    """A prompt in chunks, then steps whose bound of the lengths grows past where another kernel is chosen: the program
+    keeps the workspace that it made for its first step."""
+    H, Hkv, D, S = 16, 2, 128, 16
+    lens = [5000, 300, 2, 77]
+    c = ref.Paged(lens, Hkv, D, S, bits)
+    cache = on_gpu(c)
+    first = batch_of(c, [1] * 4, max_new=1, max_len=5000)
+    ws = s2.cache_attention_workspace(cache, first, H)
+    for news, max_len in ([1] * 4, 5000), ([300, 300, 2, 70], 5000), ([5, 5, 2, 5], 5008), ([40, 1, 1, 1], 5008), ([1] * 4, 0):
+        batch = batch_of(c, news, max_new=max(news), max_len=max_len)
+        q = torch.randn(sum(news), H, D, generator=torch.Generator().manual_seed(max_len)).bfloat16()
+        o, _, to, _ = ref.attention(c, q, starts_of(news))
+        got = s2.cache_attention(cache, batch, q.cuda(), workspace=ws)
+        assert ((got.double().cpu() - o).abs() <= to).all()
+    s2.check_status()
