@@ -44,7 +44,8 @@ struct Seq {
   int first, n, len;
 };
 
-// A sequence whose numbers are out of range is reported and left out (n = 0).
+// A sequence whose numbers are out of range is reported and left out (n = 0).  One without new tokens takes no part, and
+// its length may be anything.
 __device__ __forceinline__ Seq load_seq(const CacheArgs& c, int b) {
   Seq s;
   const int lo = c.starts ? c.starts[b] : b;
@@ -52,11 +53,11 @@ __device__ __forceinline__ Seq load_seq(const CacheArgs& c, int b) {
   s.len = c.lens[b];
   s.first = lo;
   s.n = hi - lo;
-  if (lo < 0 || hi < lo || hi > c.T || s.len < 0 || (long long)s.len > ((long long)c.width << c.log2s)) {
-    atomicOr(c.status, kCacheFlag);
-    s.n = 0;
-    s.len = 0;
-  }
+  // (no short circuits: the length is asked for along with the starts, not after them)
+  const bool beyond = (s.len < 0) | ((long long)s.len > ((long long)c.width << c.log2s));
+  const bool bad = (lo < 0) | (hi < lo) | (hi > c.T) | ((hi > lo) & beyond);
+  if (bad) atomicOr(c.status, kCacheFlag);
+  if (bad | (hi == lo)) s.n = s.len = 0;
   return s;
 }
 

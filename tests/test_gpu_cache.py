@@ -672,3 +672,25 @@ def test_one_workspace_over_a_conversation(bits):
         got = s2.cache_attention(cache, batch, q.cuda(), workspace=ws)
         assert ((got.double().cpu() - o).abs() <= to).all()
     s2.check_status()
+
+
+@pytest.mark.parametrize("H,wide", [(4, False), (48, True)])
+@pytest.mark.parametrize("length", [-1, 10 ** 6, 2 ** 31 - 1])
+def test_sequences_without_new_tokens_take_no_part(length, H, wide):
+    # a slot that no conversation holds: neither its length nor its pages are looked at
+    c = ref.Paged([40, 33, 64], 2, 64, 16, 16)
+    news = [2, 0, 1]
+    q = torch.randn(3, H, 64, generator=torch.Generator().manual_seed(H)).bfloat16()
+    o, _, to, _ = ref.attention(c, q, starts_of(news))
+    c.lens[1] = length
+    c.table[1] = -7
+    for hints in (dict(max_new=2), dict(max_new=2, max_len=64)):
+        cache, batch = on_gpu(c), batch_of(c, news, wide=wide, **hints)
+        got = s2.cache_attention(cache, batch, q.cuda())
+        s2.check_status()
+        assert ((got.double().cpu() - o).abs() <= to).all()
+        x = torch.randn(3, 2, 64).bfloat16().cuda()
+        s2.cache_append(cache, batch, x, x, base=0.0)
+        k, _ = s2.cache_read(cache, batch)
+        s2.check_status()
+        assert torch.equal(k, x)
