@@ -81,6 +81,17 @@ __device__ __forceinline__ float2 q4_pair(uint32_t raw) {
   return make_float2(__uint_as_float(raw << 16), __uint_as_float(raw & 0xffff0000u));
 }
 
+// A key's part in a score, s·(q·(128 + c)) + (m - 128 s)·sum(q), goes through numbers that are up to 19 times the largest
+// of the row, so for a row near the end of 32 bits they would leave it.  The kernels work on 2^-5 of the score instead
+// (exact: only powers of two), which scale_log2 makes up for:
+//   (2^-5 s)·(q·(128 + c)) + (2^-12 m - 2^-5 s)·(128 sum(q)).
+constexpr float kQ4ScoreUnit = 32.f, kQ4Bias = 128.f;
+// {2^-5 s, 2^-12 m - 2^-5 s} of a key's (s, m).
+__device__ __forceinline__ float2 q4_key(float2 pair) {
+  const float s = pair.x * (1.f / kQ4ScoreUnit);
+  return make_float2(s, fmaf(pair.y, 1.f / (kQ4ScoreUnit * kQ4Bias), -s));
+}
+
 // ---------------------------------------------------------------- cutting the work into equal pieces
 // All sequences' work, weighed by `weight(b)`, forms one line that is cut into
 // equal pieces, one per CTA.  The lengths are only known on the device, so

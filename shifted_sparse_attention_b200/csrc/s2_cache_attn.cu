@@ -3,7 +3,7 @@
 // For new token t of sequence b at place p, head h of key/value head h / g:
 //     o = sum_{j <= p} softmax_j(q·k_j / sqrt(D)) v_j,   lse = ln sum exp.
 // From a 4-bit cache, with k_j = mk + sk·ck:
-//     q·k_j       = sk (q·(128 + ck_j)) + (mk - 128 sk) sum(q),
+//     q·k_j       = sk (q·(128 + ck_j)) + (mk - 128 sk) sum(q)  (and 2^-5 of it: s2_cache.cuh),
 //     sum p_j v_j = sum (p_j sv_j)(cv_j - 8) + sum p_j (mv_j + 8 sv_j),
 // so the matrix products see whole numbers, which bf16 holds as they are, and
 // nothing of a row is rounded (values centred: rounded weights then meet small
@@ -310,7 +310,7 @@ __global__ void __launch_bounds__(W * 32, ctas_per_sm<Q4, NR, W>())
         sum += __shfl_xor_sync(0xffffffffu, sum, 1);
         sum += __shfl_xor_sync(0xffffffffu, sum, 2);
 #pragma unroll
-        for (int e = 0; e < 2; ++e) qsum[y][e] = __shfl_sync(0xffffffffu, sum, (2 * cc + e) * 4);
+        for (int e = 0; e < 2; ++e) qsum[y][e] = kQ4Bias * __shfl_sync(0xffffffffu, sum, (2 * cc + e) * 4);
       } else {
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) {
@@ -417,12 +417,11 @@ __global__ void __launch_bounds__(W * 32, ctas_per_sm<Q4, NR, W>())
           if constexpr (Q4) {
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
-              const float2 pr = q4_pair(kr[u].pair[t]);
-              const float mid = fmaf(-128.f, pr.x, pr.y);
+              const float2 pr = q4_key(q4_pair(kr[u].pair[t]));
 #pragma unroll
               for (int y = 0; y < NR; ++y)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) s[y][u][2 * t + e] = fmaf(s[y][u][2 * t + e], pr.x, mid * qsum[y][e]);
+                for (int e = 0; e < 2; ++e) s[y][u][2 * t + e] = fmaf(s[y][u][2 * t + e], pr.x, pr.y * qsum[y][e]);
             }
           }
         }

@@ -24,7 +24,7 @@
 // 4 bits: packed rows come by bulk copies and are unpacked to whole numbers
 // that bf16 holds as they are, 128 + code for keys (no subtraction) and code - 8
 // for values (so that rounded weights meet small numbers).  The softmax applies
-// scale and min of each key: s = sk (q·k') + (mk - 128 sk) sum(q); the weight that
+// scale and min of each key: s = sk (q·k') + (mk - 128 sk) sum(q) (2^-5 of it, s2_cache.cuh); the weight that
 // goes into the product is p·sv (rounded to bf16, relative 2^-9), and
 // sum p (mv + 8 sv), the same for every channel, is kept beside O.
 // Measured: 2048 tokens (32 heads, 8 key heads, D 128) over 16384 keys 435
@@ -643,11 +643,11 @@ do {                                                                            
         for (int y = 0; y < 2; ++y) {
           const int row = tid + 64 * y;
           const uint32_t* pairs = reinterpret_cast<const uint32_t*>(smem + L::kRaw + rs * L::kRawBytes + kT * D);
-          const float2 k2 = q4_pair(row < used ? pairs[row] : 0u), v2 = q4_pair(row < used ? pairs[kT + row] : 0u);
+          const float2 k2 = q4_key(q4_pair(row < used ? pairs[row] : 0u)), v2 = q4_pair(row < used ? pairs[kT + row] : 0u);
           // {scale, scale, min, min} of two keys: adjacent registers for the softmax's packed arithmetic
           float* to = reinterpret_cast<float*>(smem + L::kScale) + sc * 4 * kT + (row / 2) * 4 + row % 2;
           to[0] = k2.x;
-          to[2] = fmaf(-128.f, k2.x, k2.y);  // codes come as 128 + code,
+          to[2] = k2.y;  // codes come as 128 + code,
           to[2 * kT] = v2.x;
           to[2 * kT + 2] = fmaf(8.f, v2.x, v2.y);  // and as code - 8
         }
@@ -698,6 +698,7 @@ do {                                                                            
             for (int z = 0; z < 4; ++z)
               qsum += __uint_as_float(w[z] << 16) + __uint_as_float(w[z] & 0xffff0000u);
           }
+          qsum *= kQ4Bias;
         }
         mbar_arrive(bar(Q_EMPTY));
       }

@@ -103,7 +103,7 @@ struct AttnIn {
   void* cuts;        // and, for many rows, before them what each piece cuts (JoinCut, s2_cache_join.cuh)
   int64_t ldq;
   int heads, g;      // query heads, and query heads of a key/value head
-  float scale_log2;  // log2(e) / sqrt(D)
+  float scale_log2;  // log2(e) / sqrt(D), of what the kernels take for a score
   int pieces, min_piece;
   int cluster;       // CTAs that share a unit where units are not cut
 };

@@ -694,3 +694,18 @@ def test_sequences_without_new_tokens_take_no_part(length, H, wide):
         k, _ = s2.cache_read(cache, batch)
         s2.check_status()
         assert torch.equal(k, x)
+
+
+@pytest.mark.parametrize("path", PATHS)
+@pytest.mark.parametrize("D", [128, 64])
+@pytest.mark.parametrize("power", [123, 120, 100, 0, -100])
+def test_four_bit_keys_of_all_sizes(D, power, path):
+    # rows up to 2^127 wide: their scale times 128, which the products go through, is beyond 32 bits
+    lens, news = [700, 33], [3, 1]
+    c = ref.Paged(lens, 2, D, 16, 4, seed=D)
+    c.ks *= 2.0 ** power
+    H = 48 if path == "many" else 6
+    q = (torch.randn(4, H, D, generator=torch.Generator().manual_seed(7)) * 2.0 ** -power).bfloat16()
+    check_not_finite(c, news, H, q, **hints_of(path, lens, news))
+    rows, _ = s2.cache_read(on_gpu(c), batch_of(c, lens))
+    assert rows.isfinite().all()
