@@ -25,7 +25,7 @@
 // that bf16 holds as they are, 128 + code for keys (no subtraction) and code - 8
 // for values (so that rounded weights meet small numbers).  The softmax applies
 // scale and min of each key: s = sk (q·k') + (mk - 128 sk) sum(q) (2^-5 of it, s2_cache.cuh); the weight that
-// goes into the product is p·sv (rounded to bf16, relative 2^-9), and
+// goes into the product is p·sv (rounded once to bf16, relative 2^-8), and
 // sum p (mv + 8 sv), the same for every channel, is kept beside O.
 // Measured: 2048 tokens (32 heads, 8 key heads, D 128) over 16384 keys 435
 // to 446 us, 1170 TFLOP/s (the products alone would take 312): the softmax's hand-off
@@ -768,12 +768,15 @@ do {                                                                            
             const bool grow = m_new > m_used + 8.0f;
             float f = 1.f;
             if (grow) {
-              f = ex2(m_used - m_new);
+              // to a whole number: the factor is a power of two, so the first half's weights below, which are bf16
+              // already, are scaled exactly and not rounded again
+              const float m_to = ceilf(m_new);
+              f = ex2(m_used - m_to);
               l *= f;
               vsum *= f;
               factor *= f;
               need = true;
-              m_used = m_new;
+              m_used = m_to;
             }
             if (half == 1 && __any_sync(0xffffffffu, grow)) {  // the first half's weights have been written already
               uint32_t w[32];

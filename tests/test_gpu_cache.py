@@ -582,6 +582,11 @@ def check_not_finite(c, news, H, q, **kw):
 PATHS = ["whole", "cut", "many"]
 
 
+def heads_of(path, news, few):
+    """Query heads (on two key heads) with which the path is taken: rows enough for the kernel for many."""
+    return few if path != "many" else 128 if max(news) < 16 else 48
+
+
 def hints_of(path, lens, news):
     return {"whole": dict(max_new=max(news), max_len=min(max(lens), 512)), "cut": dict(max_new=max(news)),
             "many": dict(max_new=max(news), wide=True)}[path]
@@ -593,7 +598,7 @@ def hints_of(path, lens, news):
                                        ([129], [2]), ([9000], [300])])
 def test_a_query_that_holds_nan(bits, lens, news, path):
     c = ref.Paged(lens, 2, 128, 16, bits, seed=lens[0])
-    T, H = sum(news), 48 if path == "many" else 6
+    T, H = sum(news), heads_of(path, news, 6)
     q = torch.randn(T, H, 128, generator=torch.Generator().manual_seed(T)).bfloat16()
     q[T - 1, H - 2, 77] = float("nan")  # one row, on the second key head
     got, _, _, _ = check_not_finite(c, news, H, q, **hints_of(path, lens, news))
@@ -614,7 +619,7 @@ def test_a_key_that_holds_nan(bits, lens, news, at, path):
         c.k[page, 1, at % 16, 5] = float("nan")
     else:
         c.ks[page, 1, at % 16] = float("nan")
-    H = 48 if path == "many" else 4
+    H = heads_of(path, news, 4)
     q = torch.randn(sum(news), H, 128, generator=torch.Generator().manual_seed(at)).bfloat16()
     got, _, _, _ = check_not_finite(c, news, H, q, **hints_of(path, lens, news))
     seen = lens[0] - news[0] + torch.arange(news[0]) >= at
@@ -630,7 +635,7 @@ def test_scores_that_are_infinite(lens, news, at, path):
     """A key with an infinity meets queries of both signs in its channel: a score of inf makes lse inf and o NaN
     (inf / inf), one of -inf has no weight, and where all are -inf, o is 0 / 0 and lse -inf."""
     c = ref.Paged(lens, 2, 128, 16, 16, seed=lens[0])
-    H, T = 48 if path == "many" else 4, sum(news)
+    H, T = heads_of(path, news, 4), sum(news)
     q = torch.randn(T, H, 128, generator=torch.Generator().manual_seed(at[0])).bfloat16()
     q[:, ::2, 0], q[:, 1::2, 0] = 1.0, -1.0
     # what the keys of score -inf leave: as if it were about -1000 / sqrt(128) = -88, a weight below 2^-100
@@ -674,7 +679,7 @@ def test_one_workspace_over_a_conversation(bits):
     s2.check_status()
 
 
-@pytest.mark.parametrize("H,wide", [(4, False), (48, True)])
+@pytest.mark.parametrize("H,wide", [(4, False), (128, True)])
 @pytest.mark.parametrize("length", [-1, 10 ** 6, 2 ** 31 - 1])
 def test_sequences_without_new_tokens_take_no_part(length, H, wide):
     # a slot that no conversation holds: neither its length nor its pages are looked at
@@ -704,8 +709,31 @@ def test_four_bit_keys_of_all_sizes(D, power, path):
     lens, news = [700, 33], [3, 1]
     c = ref.Paged(lens, 2, D, 16, 4, seed=D)
     c.ks *= 2.0 ** power
-    H = 48 if path == "many" else 6
+    H = heads_of(path, news, 6)
     q = (torch.randn(4, H, D, generator=torch.Generator().manual_seed(7)) * 2.0 ** -power).bfloat16()
     check_not_finite(c, news, H, q, **hints_of(path, lens, news))
     rows, _ = s2.cache_read(on_gpu(c), batch_of(c, lens))
     assert rows.isfinite().all()
+
+
+@pytest.mark.parametrize("first,second,scale,value", [  # largest errors among the bf16 numbers, were both roundings made
+    (39.25, 50.0, 1.9609375, 5), (42.5, 44.75, 1.3359375, 4), (43.75, 50.0, 1.1171875, 6),
+])
+def test_four_bit_weights_are_rounded_once(first, second, scale, value):
+    """The kernel for many rows writes the weights of a tile's first half before it knows the second half's maximum.
+    Where that grows, they are scaled down, which must not round them again: all weight is the first half's here."""
+    c = ref.Paged([256], 1, 64, 128, 4)
+    pages = c.table[0, :2].long()
+    score = torch.zeros(2, 128)
+    score[1, :64], score[1, 64:] = first, second  # over sqrt(64): in powers of two 0, 7.1 to 7.9, 8.1 to 9
+    B = 200  # so many conversations with the same pages that many are not cut between their two tiles
+    c.table, c.lens = c.table.expand(B, -1).contiguous(), [256] * B
+    c.k.zero_()  # rows whose channels are all their smallest value
+    c.ks[pages, 0, :, 0], c.ks[pages, 0, :, 1] = 0.0, score.bfloat16()
+    codes = torch.full((2, 128), 8, dtype=torch.uint8)
+    codes[1, :64] += value
+    c.v[pages, 0] = (codes | codes << 4)[..., None]
+    c.vs[pages, 0, :, 0], c.vs[pages, 0, :, 1] = scale, -8 * scale
+    q = torch.zeros(B, 64, 64).bfloat16()
+    q[..., 0] = 1.0
+    check_not_finite(c, [1] * B, 64, q, wide=True, max_new=1)
