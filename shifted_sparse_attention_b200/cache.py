@@ -9,7 +9,8 @@ over everything their sequences hold:
     o = cache_attention(cache, batch, q)
 
 Argument marshalling only; the computation runs in libs2attn.so.  Tensors that
-a call allocates itself belong to the stream that it runs on.
+a call allocates itself belong to the stream that it runs on.  There is no
+backward: tensors that want a gradient are refused outside torch.no_grad().
 """
 from __future__ import annotations
 
@@ -156,6 +157,8 @@ def _plain(cache, batch, stream):
 
 def _rows(name, t, cache, batch, heads):
     """Row stride of [tokens, heads, D] bf16 rows whose heads lie side by side."""
+    if t.requires_grad and torch.is_grad_enabled():
+        raise ValueError("%s wants a gradient, and there is none through the cache: call under torch.no_grad()" % name)
     if t.dtype is not torch.bfloat16 or t.get_device() != cache.index or t.shape != (batch.tokens, heads, cache.dim):
         raise ValueError("%s must be bf16 [%d, %d, %d] on the cache's device" % (
             name, batch.tokens, heads, cache.dim))

@@ -122,6 +122,22 @@ def test_tensor_helpers_refuse_host_tensors(abi):
         s2.CacheBatch(t, t[:, 0])
 
 
+def test_tensors_that_want_a_gradient_are_refused():
+    """There is no backward: a result without a gradient must not come in silence."""
+    from types import SimpleNamespace
+    from shifted_sparse_attention_b200.cache import _rows
+    cache, batch = SimpleNamespace(index=-1, dim=64), SimpleNamespace(tokens=3)  # -1: host tensors
+    leaf = torch.zeros(3, 2, 64, dtype=torch.bfloat16, requires_grad=True)
+    for t in (leaf, leaf * 2):
+        with pytest.raises(ValueError, match="gradient"):
+            _rows("q", t, cache, batch, 2)
+        with torch.no_grad():
+            assert _rows("q", t, cache, batch, 2) == 128
+        assert _rows("q", t.detach(), cache, batch, 2) == 128
+    with torch.inference_mode():
+        assert _rows("q", leaf * 2, cache, batch, 2) == 128
+
+
 def test_reference_rows_of_four_bits():
     x = torch.randn(50, 128, generator=torch.Generator().manual_seed(0)).bfloat16()
     c, s, m = ref.pack(x)
