@@ -192,15 +192,17 @@ __device__ __forceinline__ int row_blocks(int n, int g) {
   return (int)(((long long)n * g + 8 * NR - 1) / (8 * NR));
 }
 
+// Warps of a CTA.
+constexpr int kW = 4;
+
 // A unit takes kUnitSteps + steps of the line: what starting and ending it costs, then its steps.
 // (Without the first, a piece of many short sequences took several times as long as the others.)
-template <int W>
-__host__ __device__ constexpr int unit_steps() { return 2 * W; }
+constexpr int kUnitSteps = 2 * kW;
 
-template <int NR, int W>
+template <int NR>
 __device__ __forceinline__ long long seq_steps(const CacheArgs& c, const AttnIn& in, int b, int step, bool cut) {
   const Seq s = load_seq(c, b);
-  return (long long)c.heads * row_blocks<NR>(s.n, in.g) * (cut ? steps_of(s.len, step) + unit_steps<W>() : 1);
+  return (long long)c.heads * row_blocks<NR>(s.n, in.g) * (cut ? steps_of(s.len, step) + kUnitSteps : 1);
 }
 
 }  // namespace
@@ -209,40 +211,40 @@ __device__ __forceinline__ long long seq_steps(const CacheArgs& c, const AttnIn&
 template <bool Q4>
 __host__ __device__ constexpr int step_blocks() { return Q4 ? 2 : 1; }
 
-// CTAs of W warps on an SM: 12 warps of 168 registers for bf16 rows (16 of 128 spill: one sequence of 32768 keys took
+// CTAs on an SM: 12 warps of 168 registers for bf16 rows (16 of 128 spill: one sequence of 32768 keys took
 // 28.7 us and not 23.1), 16 of 128 for 4-bit ones, 8 of 255 with two blocks of query rows.
-template <bool Q4, int NR, int W>
-__host__ __device__ constexpr int ctas_per_sm() { return (NR == 2 ? 8 : Q4 ? 16 : 12) / W; }
+template <bool Q4, int NR>
+__host__ __device__ constexpr int ctas_per_sm() { return (NR == 2 ? 8 : Q4 ? 16 : 12) / kW; }
 
 constexpr int kMaxCluster = 8;
 
-template <int D, int NR, int W>
+template <int D, int NR>
 struct DecodeShared {
-  long long line[W + 2];
+  long long line[kW + 2];
   long long x0, x1;  // the CTA's piece [x0, x1) of the line: here and not in registers, which the keys need
-  float m[W][8 * NR], l[W][8 * NR], div[W][8 * NR];  // maximum, sum of weights, what O is divided by
+  float m[kW][8 * NR], l[kW][8 * NR], div[kW][8 * NR];  // maximum, sum of weights, what O is divided by
   alignas(16) float4 all[8 * NR];                    // the same of the CTA, for its cluster (O is then in o[0])
-  alignas(16) float o[W][8 * NR][D + 4];
+  alignas(16) float o[kW][8 * NR][D + 4];
 };
 
-template <int D, bool Q4, int NR, int W>
-__global__ void __launch_bounds__(W * 32, ctas_per_sm<Q4, NR, W>())
+template <int D, bool Q4, int NR>
+__global__ void __launch_bounds__(kW * 32, ctas_per_sm<Q4, NR>())
     s2_cache_decode_kernel(const __grid_constant__ CacheArgs c, const __grid_constant__ AttnIn in) {
-  constexpr int kThreads = W * 32;
+  constexpr int kThreads = kW * 32;
   constexpr int kBlocks = step_blocks<Q4>();
   constexpr int kStep = 16 * kBlocks;
   constexpr int kRows = 8 * NR;
   constexpr int kTiles = D / 16;  // 16-channel tiles of O^T
   constexpr int kRowBytes = Q4 ? D / 2 : 2 * D;
   extern __shared__ __align__(16) uint8_t smem[];
-  auto& sh = *reinterpret_cast<DecodeShared<D, NR, W>*>(smem);
+  auto& sh = *reinterpret_cast<DecodeShared<D, NR>*>(smem);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, r = lane / 4, cc = lane % 4;
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join may start its own set-up
   // cut units: each takes its steps of the line; whole units: one point each, and a CTA, or the CTAs of a cluster
   // together, take one unit
   const bool cut = in.pieces > 0;
-  auto weight = [&](int i) { return seq_steps<NR, W>(c, in, i, kStep, cut); };
+  auto weight = [&](int i) { return seq_steps<NR>(c, in, i, kStep, cut); };
   int b;
   long long seq_first;
   const int index = (int)(blockIdx.x / (unsigned)in.cluster), rank = (int)(blockIdx.x % (unsigned)in.cluster);
@@ -265,7 +267,7 @@ __global__ void __launch_bounds__(W * 32, ctas_per_sm<Q4, NR, W>())
     Seq seq = load_seq(c, b);
     const int blocks = row_blocks<NR>(seq.n, in.g);
     const int steps = steps_of(seq.len, kStep);
-    const int head = cut ? unit_steps<W>() : 0, span = cut ? steps + head : 1;
+    const int head = cut ? kUnitSteps : 0, span = cut ? steps + head : 1;
     if (x >= seq_first + (long long)c.heads * blocks * span) {  // this sequence is done
       seq_first += (long long)c.heads * blocks * span;
       ++b;
@@ -377,10 +379,10 @@ __global__ void __launch_bounds__(W * 32, ctas_per_sm<Q4, NR, W>())
       for (int u = 0; u < kBlocks; ++u) load_keys(kr[u], k_base + (size_t)rows[u] * kRowBytes, ks_base + (size_t)rows[u] * 4);
 #pragma unroll
       for (int u = 0; u < kBlocks; ++u) load_values(vr[u], v_base + (size_t)rows[u] * kRowBytes, vs_base + (size_t)rows[u] * 4);
-      for (; k < k1; k += W) {
+      for (; k < k1; k += kW) {
         const int key0 = k * kStep;
-        const bool more = k + W < k1;
-        if (more) find_rows(k + W);
+        const bool more = k + kW < k1;
+        if (more) find_rows(k + kW);
         // scores: keys r, r + 8 of each block by rows 2cc, 2cc + 1
         float s[NR][kBlocks][4];
 #pragma unroll
@@ -590,11 +592,11 @@ __global__ void __launch_bounds__(W * 32, ctas_per_sm<Q4, NR, W>())
       const int row = i / (D / 4), d = 4 * (i % (D / 4));
       float mm = sh.m[0][row];
 #pragma unroll
-      for (int w = 1; w < W; ++w) mm = fmaxf(mm, sh.m[w][row]);
+      for (int w = 1; w < kW; ++w) mm = fmaxf(mm, sh.m[w][row]);
       float ll = 0.f, div = 0.f;
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int w = 0; w < W; ++w) {
+      for (int w = 0; w < kW; ++w) {
         if (sh.l[w][row] == 0.f) continue;  // saw no key
         const float f = ex2(sh.m[w][row] - base_of(mm));
         const float4 v = *reinterpret_cast<const float4*>(&sh.o[w][row][d]);
@@ -657,14 +659,14 @@ __global__ void __launch_bounds__(W * 32, ctas_per_sm<Q4, NR, W>())
 // Joins the partial sums of units that the line's cuts run through.  CTA i
 // stands for cut i + 1; the CTAs of one unit's cuts share its rows out.  They
 // find the unit by themselves, while the sums are still being made.
-template <int D, bool Q4, int NR, int W>
+template <int D, bool Q4, int NR>
 __global__ void __launch_bounds__(kJoinThreads) s2_cache_join_kernel(const __grid_constant__ CacheArgs c,
                                                                      const __grid_constant__ AttnIn in) {
   constexpr int kStep = 16 * step_blocks<Q4>();
   constexpr int kRows = 8 * NR;
   __shared__ long long line_sh[kJoinThreads / 32 + 2];
   __shared__ JoinShared<D> sh;
-  auto weight = [&](int i) { return seq_steps<NR, W>(c, in, i, kStep, true); };
+  auto weight = [&](int i) { return seq_steps<NR>(c, in, i, kStep, true); };
   int b;
   long long seq_first;
   const Line line =
@@ -674,9 +676,9 @@ __global__ void __launch_bounds__(kJoinThreads) s2_cache_join_kernel(const __gri
   u.rows = 0;
   if (cut < line.total) {
     const Seq seq = load_seq(c, b);
-    const int steps = steps_of(seq.len, kStep), blocks = row_blocks<NR>(seq.n, in.g), span = steps + unit_steps<W>();
+    const int steps = steps_of(seq.len, kStep), blocks = row_blocks<NR>(seq.n, in.g), span = steps + kUnitSteps;
     const long long unit = quotient(cut - seq_first, span);
-    const long long first = seq_first + unit * span + unit_steps<W>();  // of its steps
+    const long long first = seq_first + unit * span + kUnitSteps;  // of its steps
     if (cut > first) {  // and not before the unit's first step
       const int h = (int)quotient(unit, blocks), rb = (int)(unit - (long long)h * blocks);
       u.rows = min(kRows, seq.n * in.g - rb * kRows);
@@ -712,22 +714,22 @@ static bool cut_units(int64_t max_len, int cluster) {
   return max_len == 0 || max_len > 256 * (cluster > 2 ? cluster : 2);
 }
 
-template <int D, bool Q4, int NR, int W>
+template <int D, bool Q4, int NR>
 static int decode_impl(const CacheArgs& c, const AttnIn& in0, int64_t max_len, cudaStream_t stream) {
   AttnIn in = in0;
   // units at most: every sequence rounds its rows up to blocks
   const int64_t rows = (int64_t)c.T * in.g / (8 * NR) + (c.T < c.B ? c.T : c.B);
   const int64_t units = c.heads * (c.starts ? rows : (int64_t)c.B * ((in.g + 8 * NR - 1) / (8 * NR)));
-  constexpr int kResident = 148 * ctas_per_sm<Q4, NR, W>();
+  constexpr int kResident = 148 * ctas_per_sm<Q4, NR>();
   in.cluster = cluster_of(units, max_len, kResident);
   const bool cut = cut_units(max_len, in.cluster);
   if (cut) in.cluster = 1;
   in.pieces = cut ? kResident : 0;
-  in.min_piece = cut ? unit_steps<W>() + W : 1;  // a step for each warp
-  constexpr int kBytes = (int)sizeof(DecodeShared<D, NR, W>);
+  in.min_piece = cut ? kUnitSteps + kW : 1;  // a step for each warp
+  constexpr int kBytes = (int)sizeof(DecodeShared<D, NR>);
   cudaError_t e;
   if (kBytes > 48 * 1024) {
-    e = cudaFuncSetAttribute(s2_cache_decode_kernel<D, Q4, NR, W>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
+    e = cudaFuncSetAttribute(s2_cache_decode_kernel<D, Q4, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
     if (e != cudaSuccess) return (int)e;
   }
   if (!cut && units >= (int64_t(1) << 31)) return (int)cudaErrorInvalidConfiguration;
@@ -737,15 +739,15 @@ static int decode_impl(const CacheArgs& c, const AttnIn& in0, int64_t max_len, c
   cfg.attrs = at;
   if (in.cluster > 1) {
     cfg.gridDim = dim3((unsigned)(units * in.cluster));
-    cfg.blockDim = dim3(W * 32);
+    cfg.blockDim = dim3(kW * 32);
     cfg.dynamicSmemBytes = kBytes;
     at[0].id = cudaLaunchAttributeClusterDimension;
     at[0].val.clusterDim.x = (unsigned)in.cluster;
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.numAttrs = 1;
-    return (int)cudaLaunchKernelEx(&cfg, s2_cache_decode_kernel<D, Q4, NR, W>, c, in);
+    return (int)cudaLaunchKernelEx(&cfg, s2_cache_decode_kernel<D, Q4, NR>, c, in);
   }
-  s2_cache_decode_kernel<D, Q4, NR, W><<<(unsigned)(cut ? in.pieces : units), W * 32, kBytes, stream>>>(c, in);
+  s2_cache_decode_kernel<D, Q4, NR><<<(unsigned)(cut ? in.pieces : units), kW * 32, kBytes, stream>>>(c, in);
   e = cudaGetLastError();
   if (e != cudaSuccess || !cut) return (int)e;
   cfg.gridDim = dim3(in.pieces - 1);
@@ -753,15 +755,15 @@ static int decode_impl(const CacheArgs& c, const AttnIn& in0, int64_t max_len, c
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.numAttrs = 1;
-  return (int)cudaLaunchKernelEx(&cfg, s2_cache_join_kernel<D, Q4, NR, W>, c, in);
+  return (int)cudaLaunchKernelEx(&cfg, s2_cache_join_kernel<D, Q4, NR>, c, in);
 }
 
 template <int D, bool Q4>
-static int decode_rows(const CacheArgs& c, const AttnIn& in, int rows, int64_t max_len, cudaStream_t stream) {
-  return rows <= 8 ? decode_impl<D, Q4, 1, 4>(c, in, max_len, stream) : decode_impl<D, Q4, 2, 4>(c, in, max_len, stream);
+static int decode_rows(const CacheArgs& c, const AttnIn& in, int64_t rows, int64_t max_len, cudaStream_t stream) {
+  return rows <= 8 ? decode_impl<D, Q4, 1>(c, in, max_len, stream) : decode_impl<D, Q4, 2>(c, in, max_len, stream);
 }
 
-int launch_cache_decode(const CacheArgs& c, const AttnIn& in, int D, bool q4, int rows, int64_t max_len,
+int launch_cache_decode(const CacheArgs& c, const AttnIn& in, int D, bool q4, int64_t rows, int64_t max_len,
                         cudaStream_t stream) {
   if (D == 64)
     return q4 ? decode_rows<64, true>(c, in, rows, max_len, stream) : decode_rows<64, false>(c, in, rows, max_len, stream);

@@ -114,7 +114,7 @@ int launch_cache_append(const CacheArgs& c, const AppendIn& in, int D, bool q4, 
 int launch_cache_read(const CacheArgs& c, int D, bool q4, void* k_out, void* v_out, cudaStream_t stream);
 // rows, max_len: query rows of a unit and a sequence's keys at most, as far as the caller knows (max_len 0: not at all);
 // they choose tiles and how units are shared out only
-int launch_cache_decode(const CacheArgs& c, const AttnIn& in, int D, bool q4, int rows, int64_t max_len,
+int launch_cache_decode(const CacheArgs& c, const AttnIn& in, int D, bool q4, int64_t rows, int64_t max_len,
                         cudaStream_t stream);
 size_t cache_decode_partial_bytes(int D);
 

@@ -218,12 +218,10 @@ int s2attn_cache_attn(const s2_cache* cache, const s2_cache_batch* batch, const 
   in.g = (int)(heads / cache->heads);
   const bool q4 = cache->format == S2_CACHE_Q4;
   in.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)D)) * (q4 ? s2::kQ4ScoreUnit : 1.f);
-  if (few_rows(cache, batch, heads)) {
-    const int64_t rows = shared_rows(cache, batch, heads);
-    return launched(s2::launch_cache_decode(a, in, (int)D, q4, rows > 16 ? 16 : (int)rows, batch->max_len,
+  if (few_rows(cache, batch, heads))
+    return launched(s2::launch_cache_decode(a, in, (int)D, q4, shared_rows(cache, batch, heads), batch->max_len,
                                             static_cast<cudaStream_t>(stream)),
                     "cache attention");
-  }
   in.cuts = workspace;
   in.partial = reinterpret_cast<float*>(static_cast<char*>(workspace) + s2::kCutBytes);
   in.pieces = s2::kChunkPieces;
