@@ -768,9 +768,12 @@ do {                                                                            
             const bool grow = m_new > m_used + 8.0f;
             float f = 1.f;
             if (grow) {
-              // to a whole number: the factor is a power of two, so the first half's weights below, which are bf16
-              // already, are scaled exactly and not rounded again
-              const float m_to = ceilf(m_new);
+              // In the second half by a whole number: the factor is a power of two (but for m_to's own rounding, too
+              // little to matter), so the first half's weights below, which are bf16 already, stay as exact as they are.
+              // Elsewhere to the maximum itself, whose key's weight is then 1 and not rounded (error of ragged 4-bit
+              // chunks 0.0022; 0.0024 with whole numbers everywhere).
+              float m_to = m_new;
+              if (half == 1 && m_used != -INFINITY) m_to = m_used + ceilf(m_new - m_used);
               f = ex2(m_used - m_to);
               l *= f;
               vsum *= f;
