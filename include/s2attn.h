@@ -291,13 +291,14 @@ int s2attn_graph_gap(const float* lse_s2, const float* lse_full, const void* o_s
  * A new token whose place is negative (seq_lens[b] < n_b, as in a padded batch
  * with seq_lens[b] = 0) has no row and sees no key: nothing is stored for it,
  * its o is 0 and its lse -inf.
- * max_new and max_len are the host's bounds of n_b and seq_lens[b]: they choose
- * kernels and their tiling, and no result depends on them.  table_width *
- * page_size < 2^30.
+ * max_new and max_len are the host's bounds of n_b and seq_lens[b].  They, and
+ * seqs, tokens and table_width, choose kernels and their tiling: results differ
+ * with them within the rounding that s2attn_cache_attn's comment names, and
+ * are right also where a bound is too low.  table_width * page_size < 2^30.
  * Numbers out of range (a page outside [0, pages), a length beyond the table, a
  * decreasing or too large start) are found by the kernels: nothing outside the
- * buffers is touched, the sequence's results are undefined, and
- * s2attn_check_status() reports S2_ERR_BOUNDS.
+ * buffers is touched, the sequence's results are undefined (of a start out of
+ * range: all sequences'), and s2attn_check_status() reports S2_ERR_BOUNDS.
  * Two sequences may share pages that are only read.  The rows of the calls'
  * inputs must not overlap their outputs. */
 enum { S2_CACHE_BF16 = 0, S2_CACHE_Q4 = 1 };
@@ -353,12 +354,19 @@ int s2attn_cache_read(const s2_cache* cache, const s2_cache_batch* batch, void* 
  * tokens * heads < 2^31), query head h reads key/value head
  * h / (heads / cache heads).  For the token at place p of its sequence
  *   o = sum_{j <= p} softmax_j(q·k_j / sqrt(D)) v_j,  lse = ln sum_{j <= p} exp(..),
- * o [tokens, heads, D] bf16, lse [tokens, heads] fp32 or NULL.  Results do not
- * depend on which other sequences are in the batch beyond the order of sums in
- * 32 bits, and are bitwise reproducible for the same batch.  Rows behind a
- * sequence's end may hold anything; a value row that is not finite makes NaN of
- * every new token of its sequence that the call computes beside it, also of
- * those before it.  workspace: s2attn_cache_attn_workspace_size bytes (0: the
+ * o [tokens, heads, D] bf16, lse [tokens, heads] fp32 or NULL.  Scores, softmax
+ * statistics and sums are in 32 bits; the weights that meet the values are
+ * rounded to bf16 (from 4 bits, weight times scale), and o once at the end.
+ * What is rounded against which running maximum, and whether the divisor is the
+ * sum of the rounded weights, is the chosen kernel's, so the other sequences of
+ * a batch and the host's bounds may change o by that rounding; the same batch
+ * gives the same bits.  Values of up to 2^100 or so (their sums, weighted by up to
+ * 2^8, stay in 32 bits).
+ * A NaN in a query or a visible key makes o and lse NaN; a score of inf makes lse
+ * inf and o NaN, and where all visible scores are -inf, o is NaN and lse -inf.  Rows
+ * behind a sequence's end may hold anything; a value row that is not finite makes
+ * NaN of every new token of its sequence that the call computes beside it, also
+ * of those before it.  workspace: s2attn_cache_attn_workspace_size bytes (0: the
  * arguments are refused), 256-byte aligned, contents on entry do not matter;
  * the size depends on D alone (40 MB at 128 channels, 21 MB at 64), so that one
  * workspace serves all batches of a program; calls that may overlap on the GPU

@@ -84,8 +84,9 @@ class CacheBatch:
     """The sequences of a call: page_table int32 [seqs, width], seq_lens int32 [seqs] (new tokens included) and
     q_starts int32 [seqs + 1], the packed starts of the new tokens (None: one per sequence), on the device;
     tokens: length of the packed axis.  max_new, max_len: the host's bounds of a sequence's new tokens and length, if
-    known; they choose kernels and change no result.  The tensors' contents are read when kernels run: the same batch
-    serves step after step, and captured graphs, while the program updates them in place."""
+    known; they choose kernels, and change results by no more than the rounding of weights to bf16.  The tensors'
+    contents are read when kernels run: the same batch serves step after step, and captured graphs, while the program
+    updates them in place."""
 
     def __init__(self, page_table, seq_lens, q_starts=None, tokens: int | None = None, max_new: int = 0,
                  max_len: int = 0):

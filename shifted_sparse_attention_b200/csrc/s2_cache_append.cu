@@ -7,7 +7,9 @@
 // rotated copy of k is written.  HBM bounds the pass into bf16 rows, the
 // rotation rides along (34,500 tokens of 32 + 8 heads of 128 channels, 848 MB:
 // 140 us); into 4-bit rows packing's instructions do (issue slots 73% taken;
-// 18,900 tokens 79 us, HBM's part 62), for a few tokens latency does.
+// 18,900 tokens 79 us, HBM's part 62), for a few tokens latency does.  Reading
+// 4-bit rows back is bound by instructions too (the same 18,900 tokens 24 us, HBM's
+// part 15; ALU 64%, issue 63%: a row's place by division, codes to numbers).
 //
 // Work: a CTA takes one token, or 4.  Their places, pages and angles come first
 // (one warp per token finds its sequence, one thread per (token, pair) its

@@ -36,9 +36,12 @@
 //   divided by the sum of the rounded ones where that is to be had (bf16 rows),
 //   so that it stays a mean of values, and lse comes from the unrounded sum.
 // Measured (D 128): 64 sequences of 17 to 8192 keys, 32 heads on 8 key heads,
-// 1.09 GB, 172 us, 0.96 of the measured copy rate; one of 32768 keys 24.8 us
+// 1.09 GB, 172 us, 0.96 of the measured copy rate; one of 32768 keys 25.2 us
 // (HBM's part 20.5); 4 bits, 48 sequences of 33 to 4096 keys, 32 key heads, 433 MB,
-// 109 us (HBM's part 66), where unpacking bounds it (ALU 57%, issue 56%).
+// 111 us (HBM's part 66).  There no pipe is near its limit (ALU 56%, issue 56%, HBM
+// 47%): of the time that a warp is not issuing, 28% goes to the fixed latencies of
+// its own last instruction, 26% to loads, 15% to other warps' turns, 14% to a busy
+// ALU, with 16 warps of 128 registers on an SM.
 #include <climits>
 
 #include <cuda_bf16.h>
@@ -706,10 +709,13 @@ static int cluster_of(int64_t units, int64_t max_len, int resident) {
 }
 
 // Whether units are cut and joined in a second launch, or whole ones taken by clusters.  The latter needs one launch and
-// no partial sums in memory, but the longest unit sets its time, and only a bound of the lengths is known: up to 256
-// keys a CTA it is no slower than the former is at half the bound on the average (us whole and cut: 32 units of 513
-// keys 7.6 and 9.5, of 1024 8.0 and 9.7, of 2048 9.9 and 12.8, of 4096 14.1 and 16.2; 8 units of 2048 8.6 and 8.7, of
-// 4096 11.3 and 9.8; 128 units, two CTAs each, of 513 10.7 and 13.4, of 2048 25.3 and 25.4).
+// no partial sums in memory, but the longest unit sets its time, and only a bound of the lengths is known.  The limits, 256
+// keys a CTA of a cluster of four or eight and 512 keys for one or two CTAs, are where it is about as fast as the former
+// with lengths of half the bound on the average (us whole and cut.  Clusters: 32 units of 513 keys 7.6 and 9.5, of 1024 8.0
+// and 9.7, of 2048 9.9 and 12.8, of 4096 14.1 and 16.2; 8 units of 2048 8.6 and 8.7, of 4096 11.3 and 9.8; 128 units, two
+// CTAs each, of 513 10.7 and 13.4, of 2048 25.3 and 25.4.  One CTA each, keys spread over 1 to 512: 512 units 18.0 and
+// 19.6, 1024 30.1 and 32.3, 2048 58.0 and 55.1, in 4 bits 13.5 and 17.7, 22.1 and 25.8, 42.0 and 41.7; over 1 to 1024, 512
+// units 31.5 and 29.0; all of 512, 512 units 32.0 and 28.4, in 4 bits 14.9 and 21.5).
 static bool cut_units(int64_t max_len, int cluster) {
   return max_len == 0 || max_len > 256 * (cluster > 2 ? cluster : 2);
 }

@@ -19,7 +19,7 @@
 // 4-7 of tile B, 8 TMA, 9 MMA issue; with 4-bit pages warps 10 and 11
 // unpack (with or without them the softmax warps have 168 registers).  MMA
 // order, TMEM layout and the softmax are those of s2_fwd.cu: S and P share columns, P feeds O += P V
-// from TMEM, and the running maximum moves in steps of 8 (in powers of two).
+// from TMEM, and the running maximum moves when a score passes it by more than 8 (in powers of two).
 //
 // 4 bits: packed rows come by bulk copies and are unpacked to whole numbers
 // that bf16 holds as they are, 128 + code for keys (no subtraction) and code - 8
@@ -27,11 +27,20 @@
 // scale and min of each key: s = sk (q·k') + (mk - 128 sk) sum(q) (2^-5 of it, s2_cache.cuh); the weight that
 // goes into the product is p·sv (rounded once to bf16, relative 2^-8), and
 // sum p (mv + 8 sv), the same for every channel, is kept beside O.
-// Measured: 2048 tokens (32 heads, 8 key heads, D 128) over 16384 keys 435
-// to 446 us, 1170 TFLOP/s (the products alone would take 312): the softmax's hand-off
-// chain bounds it (tensor pipe 56%).  4 bits, three chunks of 260 to 1000
-// tokens over 3000 to 12000 keys 333 us, bound by the softmax's work on each
-// key's scale and min.  Short calls: 60 tokens over 8000 keys 33 us, of which
+//
+// Weights are rounded to bf16 for the product (2^-8 of each at most), and O is
+// divided by their sum in 32 bits as it was before that rounding: with the sum of the rounded
+// ones, as s2_cache_attn.cu has it for bf16 rows, o's error against 64 bits is 0.00199
+// of its norm and not 0.00204, but 2048 tokens over 16384 keys take 464 us and
+// not 442, since the softmax warps set the pace.
+//
+// Measured: 2048 tokens (32 heads, 8 key heads, D 128) over 16384 keys 434
+// to 457 us by box in a captured graph, 1130 to 1190 TFLOP/s (the products alone would
+// take 312), and 502 to 520 (about 1010) called one by one, when the power cap
+// holds the clock down: the softmax's hand-off chain bounds it (tensor pipe 55%).  4 bits,
+// three chunks of 260 to 1000 tokens over 3000 to 12000 keys 336 us, where no
+// pipe is near its limit (issue 45%, tensor and XU 34%): it is the softmax warps' work on
+// each key's scale and min that is long.  Short calls: 60 tokens over 8000 keys 33 us, of which
 // finding the first segment takes 4, loading 2, the sums' way out 3, the join 10.
 #include <climits>
 
