@@ -790,7 +790,8 @@ do {                                                                            
               need = true;
               m_used = m_to;
             }
-            if (half == 1 && __any_sync(0xffffffffu, grow)) {  // the first half's weights have been written already
+            const bool any_grow = __any_sync(0xffffffffu, grow);
+            if (half == 1 && any_grow) {  // the first half's weights have been written already
               uint32_t w[32];
               tmem_wait_st();
               tmem_ld32(tS, w);
@@ -865,8 +866,10 @@ do {                                                                            
           const float2 sum = __fadd2_rn(__fadd2_rn(acc[0], acc[1]), __fadd2_rn(acc[2], acc[3]));
           l += sum.x + sum.y;
         }
+        // (a warp's lanes come together in every tile, since the accesses to tensor memory are all lanes' at once)
+        const bool any_need = __any_sync(0xffffffffu, need);
         // S(t) was issued behind O += P V of tile t - 1, so O is complete here
-        if (t > g.t0 && __any_sync(0xffffffffu, need)) {
+        if (t > g.t0 && any_need) {
 #pragma unroll
           for (int j = 0; j < D / 32; ++j) {
             uint32_t o[32];
@@ -930,6 +933,7 @@ do {                                                                            
                   make_float4(__uint_as_float(o[4 * i]) + vsum, __uint_as_float(o[4 * i + 1]) + vsum,
                               __uint_as_float(o[4 * i + 2]) + vsum, __uint_as_float(o[4 * i + 3]) + vsum);
           }
+          __syncwarp();  // before tensor memory is read again, by all lanes at once
         }
         if (live) {
           if (g.slot < 0) {
