@@ -35,7 +35,7 @@
 // not 442, since the softmax warps set the pace.
 //
 // Measured: 2048 tokens (32 heads, 8 key heads, D 128) over 16384 keys 434
-// to 457 us by box in a captured graph, 1130 to 1190 TFLOP/s (the products alone would
+// to 457 us on several GPUs in a captured graph, 1130 to 1190 TFLOP/s (the products alone would
 // take 312), and 502 to 520 (about 1010) called one by one, when the power cap
 // holds the clock down: the softmax's hand-off chain bounds it (tensor pipe 55%).  4 bits,
 // three chunks of 260 to 1000 tokens over 3000 to 12000 keys 336 us, where no
